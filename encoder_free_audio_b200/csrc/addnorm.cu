@@ -1,0 +1,244 @@
+// Residual addition and RMSNorm, with outputs in fp32, bf16 or e4m3 with scales ("Inside Inkling:
+// Audio Design", Part 3 · Inference: the decoder's residual stream, whose branch outputs pass
+// through the ShortConv):  s = x + r,  y = w s / sqrt(mean(s^2) + eps).
+//
+// Each value is read once and written once (two inputs, the stream and the normed row out): HBM
+// bound. A block owns a row at a time; each thread keeps its 8-value pieces of the row in
+// registers between the sum of squares and the scaling, so nothing is read twice but the weights
+// (which stay in L1 and L2). A piece is 16 bytes of bf16 or 32 of fp32.
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace dmel {
+namespace {
+
+constexpr float kE4m3Max = 448.0f;
+constexpr float kMinAmax = 1e-30f;  // a block of zeros gets this / 448 as its scale, never zero
+
+// 8 consecutive values. The inputs may be the outputs' buffers, so these are plain (coherent)
+// accesses; the rows are not read again, so they need no place in L1.
+__device__ __forceinline__ void load8(const float *p, float (&v)[8]) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+    asm volatile("ld.global.L1::no_allocate.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v[4 * h]), "=f"(v[4 * h + 1]), "=f"(v[4 * h + 2]), "=f"(v[4 * h + 3])
+                 : "l"(p + 4 * h)
+                 : "memory");
+}
+__device__ __forceinline__ void unpack8(const uint32_t (&u)[4], float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(u[i] << 16);
+    v[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+  }
+}
+__device__ __forceinline__ void load8(const __nv_bfloat16 *p, float (&v)[8]) {
+  uint32_t u[4];
+  asm volatile("ld.global.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3])
+               : "l"(p)
+               : "memory");
+  unpack8(u, v);
+}
+__device__ __forceinline__ void weight8(const float *p, float (&v)[8]) {
+  const float4 a = __ldg(reinterpret_cast<const float4 *>(p)), b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
+  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+}
+__device__ __forceinline__ void weight8(const __nv_bfloat16 *p, float (&v)[8]) {
+  const uint4 q = __ldg(reinterpret_cast<const uint4 *>(p));
+  const uint32_t u[4] = {q.x, q.y, q.z, q.w};
+  unpack8(u, v);
+}
+__device__ __forceinline__ void store8(float *p, const float (&v)[8]) {
+  reinterpret_cast<float4 *>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+  reinterpret_cast<float4 *>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+}
+__device__ __forceinline__ void store8(__nv_bfloat16 *p, const float (&v)[8]) {
+  uint32_t u[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+    u[i] = *reinterpret_cast<const uint32_t *>(&h);
+  }
+  *reinterpret_cast<uint4 *>(p) = make_uint4(u[0], u[1], u[2], u[3]);
+}
+// e4m3, nearest even, clamped to +-448 (NaN stays NaN)
+__device__ __forceinline__ void store8(__nv_fp8_e4m3 *p, const float (&v)[8]) {
+  uint32_t w[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(v[4 * h], v[4 * h + 1]), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(v[4 * h + 2], v[4 * h + 3]), __NV_SATFINITE, __NV_E4M3);
+    w[h] = lo | (hi << 16);
+  }
+  *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
+}
+
+struct Add {
+  __device__ float operator()(float a, float b) const { return a + b; }
+};
+struct Max {
+  __device__ float operator()(float a, float b) const { return fmaxf(a, b); }
+};
+
+// One value per block over its `warps` warps, the same in every thread; `slots` is this
+// reduction's own 32 floats of shared memory.
+template <typename Op>
+__device__ __forceinline__ float block_reduce(float v, float *slots, int warps, Op op) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = op(v, __shfl_xor_sync(0xffffffffu, v, o));
+  if (warps == 1) return v;
+  const int lane = threadIdx.x & 31;
+  if (lane == 0) slots[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = lane < warps ? slots[lane] : 0.0f;  // (0 is neutral: sums and magnitudes)
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = op(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+
+// V pieces of 8 values per thread: piece j of thread t holds columns 8 (j blockDim + t) and on.
+template <typename T, typename TO, int V>
+__global__ void __launch_bounds__(1024) add_rmsnorm_kernel(const T *x, const T *res, int64_t n_rows, int dim, const T *__restrict__ w, float eps,
+                                   T *res_out, TO *out, float *scales, int scale_block) {
+  __shared__ float red[2][2][32];
+  const int warps = blockDim.x >> 5, pieces = dim >> 3;
+  int turn = 0;  // two sets of slots: a row's second use of one is a barrier away from its first
+  for (int64_t row = blockIdx.x; row < n_rows; row += gridDim.x, turn ^= 1) {
+    const int64_t base = row * dim;
+    float s[V][8];
+    float ss = 0.0f;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const int p = j * blockDim.x + threadIdx.x;
+      if (p < pieces) {
+        load8(x + base + 8 * p, s[j]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s[j][i] = 0.0f;
+      }
+    }
+    if (res) {
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const int p = j * blockDim.x + threadIdx.x;
+        if (p < pieces) {
+          float r[8];
+          load8(res + base + 8 * p, r);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) s[j][i] += r[i];
+        }
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) ss = fmaf(s[j][i], s[j][i], ss);
+    }
+    if (res_out) {
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const int p = j * blockDim.x + threadIdx.x;
+        if (p < pieces) store8(res_out + base + 8 * p, s[j]);
+      }
+    }
+    ss = block_reduce(ss, red[turn][0], warps, Add());
+    const float rstd = 1.0f / sqrtf(ss / (float)dim + eps);
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const int p = j * blockDim.x + threadIdx.x;
+      if (p < pieces) {
+        float g[8];
+        weight8(w + 8 * p, g);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s[j][i] = s[j][i] * rstd * g[i];
+      }
+    }
+    if (sizeof(TO) == 1) {
+      // largest magnitude of each piece, then of its block: 4, 8 or 16 neighbouring threads (the
+      // block's pieces, since blockDim is a multiple of 32), or the whole row. fmaxf drops NaN.
+      float top[V];
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        top[j] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) top[j] = fmaxf(top[j], fabsf(s[j][i]));
+      }
+      if (scale_block == 0) {
+        float m = top[0];
+#pragma unroll
+        for (int j = 1; j < V; ++j) m = fmaxf(m, top[j]);
+        m = block_reduce(m, red[turn][1], warps, Max());
+#pragma unroll
+        for (int j = 0; j < V; ++j) top[j] = m;
+        if (threadIdx.x == 0) scales[row] = fmaxf(m, kMinAmax) / kE4m3Max;
+      } else {
+        const int per = scale_block >> 3, n_blocks = (pieces + per - 1) / per;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          for (int o = 1; o < per; o <<= 1) top[j] = fmaxf(top[j], __shfl_xor_sync(0xffffffffu, top[j], o));
+          const int p = j * blockDim.x + threadIdx.x;
+          if (p < pieces && p % per == 0) scales[row * n_blocks + p / per] = fmaxf(top[j], kMinAmax) / kE4m3Max;
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const float scale = fmaxf(top[j], kMinAmax) / kE4m3Max;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s[j][i] = s[j][i] / scale;
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const int p = j * blockDim.x + threadIdx.x;
+      if (p < pieces) store8(out + base + 8 * p, s[j]);
+    }
+  }
+}
+
+template <typename T, typename TO>
+cudaError_t launch_typed(const void *x, const void *res, int64_t n_rows, int dim, const void *w, float eps,
+                         void *res_out, void *out, float *scales, int scale_block, int num_sms, cudaStream_t stream) {
+  // up to 1024 threads with one piece each, or two pieces for rows above 8192 values
+  const int pieces = dim / 8, v = pieces > 1024 ? 2 : 1;
+  const int threads = ((pieces + v - 1) / v + 31) / 32 * 32;
+  const int64_t cap = (int64_t)num_sms * 64;
+  const unsigned grid = (unsigned)(n_rows < cap ? n_rows : cap);
+  const T *xt = static_cast<const T *>(x), *rt = static_cast<const T *>(res), *wt = static_cast<const T *>(w);
+  T *so = static_cast<T *>(res_out);
+  TO *ot = static_cast<TO *>(out);
+  if (v == 1)
+    add_rmsnorm_kernel<T, TO, 1><<<grid, threads, 0, stream>>>(xt, rt, n_rows, dim, wt, eps, so, ot, scales, scale_block);
+  else
+    add_rmsnorm_kernel<T, TO, 2><<<grid, threads, 0, stream>>>(xt, rt, n_rows, dim, wt, eps, so, ot, scales, scale_block);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_add_rmsnorm(const void *x, const void *residual, int64_t n_rows, int dim, dmel_dtype dtype,
+                               const void *w, float eps, void *residual_out, void *out, dmel_dtype out_dtype,
+                               float *scales, int scale_block, int num_sms, cudaStream_t stream, int *launches) {
+#define DMEL_NORM(T, TO) \
+  launch_typed<T, TO>(x, residual, n_rows, dim, w, eps, residual_out, out, scales, scale_block, num_sms, stream)
+  cudaError_t e;
+  if (dtype == DMEL_BF16)
+    e = out_dtype == DMEL_E4M3   ? DMEL_NORM(__nv_bfloat16, __nv_fp8_e4m3)
+        : out_dtype == DMEL_BF16 ? DMEL_NORM(__nv_bfloat16, __nv_bfloat16)
+                                 : DMEL_NORM(__nv_bfloat16, float);
+  else
+    e = out_dtype == DMEL_E4M3   ? DMEL_NORM(float, __nv_fp8_e4m3)
+        : out_dtype == DMEL_BF16 ? DMEL_NORM(float, __nv_bfloat16)
+                                 : DMEL_NORM(float, float);
+#undef DMEL_NORM
+  if (e == cudaSuccess) ++*launches;
+  return e;
+}
+
+}  // namespace dmel

@@ -391,6 +391,136 @@ dmel_status dmel_shortconv(const void *x, const int64_t *seq_offsets, int n_seq,
 }
 
 namespace {
+// A buffer of an entry point's arguments, for the overlap rules.
+struct Span {
+  const void *p;
+  size_t bytes;
+};
+bool overlaps(Span a, Span b) {
+  const uintptr_t pa = reinterpret_cast<uintptr_t>(a.p), pb = reinterpret_cast<uintptr_t>(b.p);
+  return a.p && b.p && a.bytes && b.bytes && pa < pb + b.bytes && pb < pa + a.bytes;
+}
+}  // namespace
+
+dmel_status dmel_add_rmsnorm(const void *x, const void *residual, int64_t n_rows, int dim, dmel_dtype dtype,
+                             const void *rms_weight, float eps, void *residual_out, void *out, dmel_dtype out_dtype,
+                             float *scales, int scale_block, dmel_stream_t stream) {
+  t_last_launches = 0;
+  if (n_rows < 0 || dim <= 0 || dim % 8 != 0 || dim > 16384 || !dtype_ok(dtype)) return DMEL_ERR_INVALID_ARG;
+  const bool e4m3 = out_dtype == DMEL_E4M3;
+  if (!dtype_ok(out_dtype) && !e4m3) return DMEL_ERR_INVALID_ARG;
+  if (!(eps > 0.0f) || !std::isfinite(eps)) return DMEL_ERR_INVALID_ARG;
+  if (scale_block != 0 && !(e4m3 && (scale_block == 32 || scale_block == 64 || scale_block == 128)))
+    return DMEL_ERR_INVALID_ARG;
+  if (n_rows > (int64_t)1 << 40) return DMEL_ERR_INVALID_ARG;  // byte counts stay far inside 64 bits
+  if (n_rows == 0) return DMEL_OK;
+  if (!x || !rms_weight || !out || (e4m3 ? !scales : scales != nullptr)) return DMEL_ERR_INVALID_ARG;
+  if (!aligned(x, 16) || !aligned(rms_weight, 16) || !aligned(out, e4m3 ? 8 : 16) || !aligned(residual, 16) ||
+      !aligned(residual_out, 16) || !aligned(scales, 4))
+    return DMEL_ERR_INVALID_ARG;
+  const size_t n = (size_t)n_rows * (size_t)dim, es = dtype == DMEL_BF16 ? 2 : 4;
+  const size_t os = e4m3 ? 1 : out_dtype == DMEL_BF16 ? 2 : 4;
+  const size_t blocks = scale_block ? ((size_t)dim + scale_block - 1) / scale_block : 1;
+  const Span in[3] = {{x, n * es}, {residual, n * es}, {rms_weight, (size_t)dim * es}};
+  const Span o[3] = {{residual_out, n * es}, {out, n * os}, {scales, (size_t)n_rows * blocks * 4}};
+  for (int i = 0; i < 3; ++i) {
+    for (int j = 0; j < 3; ++j) {
+      // each thread reads the elements it overwrites first, so the same buffer of the same type is fine
+      const bool same = i < 2 && j < 2 && o[i].p == in[j].p && o[i].bytes == in[j].bytes;
+      if (overlaps(o[i], in[j]) && !same) return DMEL_ERR_INVALID_ARG;
+    }
+    for (int j = i + 1; j < 3; ++j)
+      if (overlaps(o[i], o[j])) return DMEL_ERR_INVALID_ARG;
+  }
+  DeviceInfo d;
+  if (device_info(&d) != cudaSuccess) return DMEL_ERR_CUDA;
+  if (d.major != 10) return DMEL_ERR_UNSUPPORTED;
+  int launches = 0;
+  const cudaError_t e = launch_add_rmsnorm(x, residual, n_rows, dim, dtype, rms_weight, eps, residual_out, out,
+                                           out_dtype, scales, scale_block, d.sms,
+                                           reinterpret_cast<cudaStream_t>(stream), &launches);
+  t_last_launches = launches;
+  return from_cuda(e);
+}
+
+dmel_status dmel_route(const void *logits, int64_t n_tokens, dmel_dtype dtype, const float *bias, const dmel_router *r,
+                       int32_t *ids, float *weights, dmel_stream_t stream) {
+  t_last_launches = 0;
+  if (n_tokens < 0 || n_tokens > (int64_t)1 << 40 || !dtype_ok(dtype) || !r) return DMEL_ERR_INVALID_ARG;
+  if (r->n_experts < 1 || r->n_experts > 1024 || r->n_shared < 0 || r->n_shared > 31) return DMEL_ERR_INVALID_ARG;
+  if (r->n_groups < 1 || r->n_groups > 32 || r->n_experts % r->n_groups != 0) return DMEL_ERR_INVALID_ARG;
+  if (r->topk_groups < 1 || r->topk_groups > r->n_groups) return DMEL_ERR_INVALID_ARG;
+  if (r->top_k < 1 || r->top_k > r->topk_groups * (r->n_experts / r->n_groups) || r->top_k + r->n_shared > 32)
+    return DMEL_ERR_INVALID_ARG;
+  if ((r->scoring != DMEL_ROUTE_SOFTMAX && r->scoring != DMEL_ROUTE_SIGMOID) || !std::isfinite(r->scale))
+    return DMEL_ERR_INVALID_ARG;
+  if (n_tokens == 0) return DMEL_OK;
+  if (!logits || !ids || !weights) return DMEL_ERR_INVALID_ARG;
+  const size_t es = dtype == DMEL_BF16 ? 2 : 4;
+  if (!aligned(logits, es) || !aligned(bias, 4) || !aligned(ids, 4) || !aligned(weights, 4)) return DMEL_ERR_INVALID_ARG;
+  const size_t cols = (size_t)r->n_experts + r->n_shared, slots = (size_t)r->top_k + r->n_shared;
+  const Span in[2] = {{logits, (size_t)n_tokens * cols * es}, {bias, (size_t)r->n_experts * 4}};
+  const Span o[2] = {{ids, (size_t)n_tokens * slots * 4}, {weights, (size_t)n_tokens * slots * 4}};
+  if (overlaps(o[0], o[1])) return DMEL_ERR_INVALID_ARG;
+  for (const Span &a : o)
+    for (const Span &b : in)
+      if (overlaps(a, b)) return DMEL_ERR_INVALID_ARG;
+  DeviceInfo d;
+  if (device_info(&d) != cudaSuccess) return DMEL_ERR_CUDA;
+  if (d.major != 10) return DMEL_ERR_UNSUPPORTED;
+  int launches = 0;
+  const cudaError_t e = launch_route(logits, n_tokens, dtype, bias, *r, ids, weights, d.sms,
+                                     reinterpret_cast<cudaStream_t>(stream), &launches);
+  t_last_launches = launches;
+  return from_cuda(e);
+}
+
+namespace {
+bool expert_sizes_ok(int64_t n_tokens, int slots, const dmel_expert_weights *w) {
+  if (!w || n_tokens < 0 || slots < 1 || slots > 64 || n_tokens > ((int64_t)1 << 30) / slots) return false;
+  if (w->n_experts < 1 || w->n_experts > 1024) return false;
+  // (2^16 at most keeps an expert's weights inside a TMA stride and every byte count inside 64 bits)
+  if (w->dim <= 0 || w->dim % 8 != 0 || w->dim > 1 << 16) return false;
+  return w->hidden > 0 && w->hidden % 8 == 0 && w->hidden <= 1 << 16;
+}
+}  // namespace
+
+size_t dmel_experts_workspace_size(int64_t n_tokens, int slots, const dmel_expert_weights *w) {
+  if (!expert_sizes_ok(n_tokens, slots, w) || n_tokens == 0) return 0;
+  return experts_workspace_bytes(n_tokens, slots, *w);
+}
+
+dmel_status dmel_experts(const void *x, int64_t n_tokens, const int32_t *ids, const float *weights, int slots,
+                         const dmel_expert_weights *w, void *out, void *workspace, size_t workspace_bytes,
+                         dmel_stream_t stream) {
+  t_last_launches = 0;
+  if (!expert_sizes_ok(n_tokens, slots, w)) return DMEL_ERR_INVALID_ARG;
+  if (n_tokens == 0) return DMEL_OK;
+  if (!x || !ids || !weights || !out || !w->w_in || !w->w_out) return DMEL_ERR_INVALID_ARG;
+  if (!aligned(x, 16) || !aligned(ids, 4) || !aligned(weights, 4) || !aligned(out, 16) || !aligned(w->w_in, 16) ||
+      !aligned(w->w_out, 16))
+    return DMEL_ERR_INVALID_ARG;
+  const size_t need = experts_workspace_bytes(n_tokens, slots, *w);
+  if (!workspace || workspace_bytes < need || !aligned(workspace, 256)) return DMEL_ERR_INVALID_ARG;
+  const size_t xb = (size_t)n_tokens * w->dim * 2, sb = (size_t)n_tokens * slots * 4;
+  const size_t wb = (size_t)w->n_experts * w->dim * w->hidden * 2;
+  const Span in[5] = {{x, xb}, {ids, sb}, {weights, sb}, {w->w_in, 2 * wb}, {w->w_out, wb}};
+  const Span o[2] = {{out, xb}, {workspace, need}};
+  if (overlaps(o[0], o[1])) return DMEL_ERR_INVALID_ARG;
+  for (const Span &a : o)
+    for (const Span &b : in)
+      if (overlaps(a, b)) return DMEL_ERR_INVALID_ARG;
+  DeviceInfo d;
+  if (device_info(&d) != cudaSuccess) return DMEL_ERR_CUDA;
+  if (d.major != 10) return DMEL_ERR_UNSUPPORTED;
+  int launches = 0;
+  const cudaError_t e = launch_experts(x, n_tokens, ids, weights, slots, *w, out, workspace, d.err, d.sms,
+                                       reinterpret_cast<cudaStream_t>(stream), &launches);
+  t_last_launches = launches;
+  return from_cuda(e);
+}
+
+namespace {
 bool hmlp_weights_ok(const dmel_hmlp_weights *w) {
   if (!w) return false;
   const int dims[4] = {w->d1, w->d2, w->d3, w->dim};

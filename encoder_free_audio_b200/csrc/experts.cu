@@ -1,0 +1,527 @@
+// The experts' gated products of the decoder's mixture-of-experts block ("Inside Inkling: Audio
+// Design", Part 3 · Inference: 256 routed and 2 shared experts, 6 chosen per token):
+//     out[t] = sum_j weights[t, j] (silu(x[t] G_e) * (x[t] U_e)) D_e,   e = ids[t, j].
+//
+// Four launches: a plan (the slots ordered by expert, cut into tiles of tokens), the gate and up
+// products with the gating in the epilogue, the down product, and each token's weighted sum.
+//
+// Both products run on the tensor cores with the roles swapped: an expert's weights are the M
+// side (256 weight columns per pair of CTAs) and its tokens the N side, whose size an MMA takes in
+// steps of 16. So an expert with 5 tokens costs a 16-wide MMA and streams its weights once, one
+// with 700 costs three tiles of about 240, and no tile is padded by more than 15 tokens.
+//
+// A product kernel is persistent, one CTA pair per two SMs: a TMA warp loads weight boxes (64
+// columns x 64 K, MN-major, 128-byte swizzle) and gathers token rows four at a time (K-major) by
+// their index, so tokens are never copied into expert order; one thread issues M = 256, K = 16
+// MMAs into a double-buffered TMEM accumulator; four warps move finished accumulators (a lane per
+// weight column) through shared memory into rows.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace dmel {
+namespace {
+
+constexpr unsigned kAll = 0xffffffffu;
+
+// One tile of tokens: rows [row0, row0 + rows) of the expert-ordered slots, all of one expert;
+// `width` is rows rounded up to the MMA's step of 16.
+struct TokenTile {
+  int expert, row0, rows, width;
+};
+
+// ---------------------------------------------------------------- plan
+//
+// The slots in expert order, stable, by counting: warp w counts its chunk of slots per expert, a
+// scan over (expert, warp) turns the counts into row numbers, and the same walk hands them out.
+// One block: at 24,576 slots it takes a few microseconds against about a millisecond of products.
+constexpr int kPlanThreads = 1024;
+
+struct PlanOut {
+  int *n_tiles;      // [1]
+  TokenTile *tiles;
+  int *token;        // [n_slots] row -> token
+  int *row;          // [n_slots] slot -> row, -1 for a slot without an expert
+};
+
+__global__ void __launch_bounds__(kPlanThreads) experts_plan_kernel(const int32_t *__restrict__ ids, int n_slots,
+                                                                    int slots, int E, int tile_tokens, PlanOut out,
+                                                                    uint32_t *err) {
+  extern __shared__ int hist[];  // [32 warps][E], then the experts' first rows [E]
+  __shared__ unsigned long long warp_sum[32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int *first = hist + 32 * E;
+  for (int i = threadIdx.x; i < 32 * E; i += kPlanThreads) hist[i] = 0;
+  __syncthreads();
+  const int chunk = ((n_slots + 31) / 32 + 31) / 32 * 32;  // slots per warp (n_slots <= 2^30)
+  const int begin = warp * chunk < n_slots ? warp * chunk : n_slots;
+  const int end = n_slots - begin < chunk ? n_slots : begin + chunk;
+  auto expert_at = [&](int i) {
+    if (i >= end) return -1;
+    const int e = ids[i];
+    return e >= 0 && e < E ? e : -1;
+  };
+  for (int i = begin; i < end; i += 32) {
+    const int e = expert_at(i + lane);
+    const unsigned peers = __match_any_sync(kAll, e);
+    if (e >= 0 && lane == __ffs(peers) - 1) hist[warp * E + e] += __popc(peers);
+    __syncwarp();
+  }
+  __syncthreads();
+  // counts -> exclusive row offsets within the expert, per warp; and the expert's total
+  int count = 0, tiles = 0;
+  const int e_mine = threadIdx.x;  // E <= 1024
+  if (e_mine < E) {
+    for (int w = 0; w < 32; ++w) {
+      const int c = hist[w * E + e_mine];
+      hist[w * E + e_mine] = count;
+      count += c;
+    }
+    tiles = (count + tile_tokens - 1) / tile_tokens;
+  }
+  // exclusive scan of {tiles, rows} over the experts
+  const unsigned long long own = ((unsigned long long)tiles << 32) | (unsigned)count;
+  unsigned long long run = own;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const unsigned long long up = __shfl_up_sync(kAll, run, o);
+    if (lane >= o) run += up;
+  }
+  if (lane == 31) warp_sum[warp] = run;
+  __syncthreads();
+  if (warp == 0) {
+    unsigned long long v = warp_sum[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned long long up = __shfl_up_sync(kAll, v, o);
+      if (lane >= o) v += up;
+    }
+    warp_sum[lane] = v;
+  }
+  __syncthreads();
+  const unsigned long long before = run - own + (warp > 0 ? warp_sum[warp - 1] : 0ull);
+  if (e_mine < E) {
+    const int row0 = (int)(unsigned)before, tile0 = (int)(before >> 32);
+    first[e_mine] = row0;
+    if (tiles > 0) {
+      const int width = ((count + tiles - 1) / tiles + 15) / 16 * 16;
+      for (int m = 0; m < tiles; ++m) {
+        const int left = count - m * width, rows = left < width ? left : width;
+        TokenTile t;
+        t.expert = e_mine;
+        t.row0 = row0 + m * width;
+        t.rows = rows;
+        t.width = (rows + 15) / 16 * 16;
+        out.tiles[tile0 + m] = t;
+      }
+    }
+  }
+  if (threadIdx.x == kPlanThreads - 1) *out.n_tiles = (int)((before + own) >> 32);
+  __syncthreads();
+  for (int i = begin; i < end; i += 32) {
+    const int e = expert_at(i + lane);
+    const unsigned peers = __match_any_sync(kAll, e);
+    int pos = -1;
+    if (e >= 0) pos = first[e] + hist[warp * E + e] + __popc(peers & ((1u << lane) - 1u));
+    __syncwarp();
+    if (e >= 0 && lane == __ffs(peers) - 1) hist[warp * E + e] += __popc(peers);
+    __syncwarp();
+    if (i + lane < end) {
+      out.row[i + lane] = pos;
+      if (pos >= 0) out.token[pos] = (i + lane) / slots;
+      else if (ids[i + lane] != -1) record_error(err, DMEL_DEVERR_EXPERT);
+    }
+  }
+}
+
+// ---------------------------------------------------------------- products (tcgen05, CTA pairs)
+//
+// kGate: D[columns x tokens] of both the gate's and the up product: each CTA's 128 M rows are 64 of
+// the gate's columns and the 64 up columns beside them, the epilogue writes bf16(silu(g) u) to
+// h [rows x hidden]. Otherwise: 128 columns of the down product per CTA, written as fp32 rows.
+template <int kTokens>
+struct EX {
+  static constexpr int BK = 64;                        // K per stage: 128 bytes of a token row
+  static constexpr int BOX = 64 * BK * 2;              // 64 columns x 64 K rows of weights: 8 KB
+  static constexpr int A_STAGE = 2 * BOX;              // this CTA's 128 M rows
+  static constexpr int B_STAGE = kTokens / 2 * BK * 2; // this CTA's half of the tokens
+  static constexpr int STG_TOKENS = 32;
+  static constexpr int STG = STG_TOKENS * 128 * 4;     // 32 tokens x 128 columns, fp32
+  static constexpr int BUDGET = 227 * 1024 - 1024 - 512 - 2 * STG;
+  static constexpr int STAGES = BUDGET / (A_STAGE + B_STAGE);
+  static constexpr int OFF_B = STAGES * A_STAGE;
+  static constexpr int OFF_STG = OFF_B + STAGES * B_STAGE;
+  static constexpr int OFF_BAR = OFF_STG + 2 * STG;
+  static constexpr int N_BARS = 2 * STAGES + 4 + 1;
+  static constexpr int SMEM_BYTES = OFF_BAR + 512 + 1024;
+  static constexpr int EPI_WARPS = 4;
+  static constexpr int THREADS = 32 * (2 + EPI_WARPS);  // warp 0 TMA, warp 1 MMA, warps 2..5 epilogue
+  static constexpr uint32_t ACC_STRIDE = kTokens;
+  static constexpr uint32_t TMEM_COLS = 2 * kTokens < 32 ? 32 : 2 * kTokens;
+  static_assert(kTokens % 32 == 0 && kTokens <= 256 && (TMEM_COLS & (TMEM_COLS - 1)) == 0, "token tile");
+  static_assert(B_STAGE % 1024 == 0 && STAGES >= 4 && STAGES <= 24, "stages");
+  static_assert(N_BARS * 8 + 8 <= 512 && SMEM_BYTES <= 227 * 1024, "shared memory budget");
+};
+
+__device__ __forceinline__ float4 silu_times(float4 g, float4 u) {
+  // __expf and __fdividef are within a few fp32 ulps here; the result is rounded to bf16
+  return make_float4(__fdividef(g.x, 1.0f + __expf(-g.x)) * u.x, __fdividef(g.y, 1.0f + __expf(-g.y)) * u.y,
+                     __fdividef(g.z, 1.0f + __expf(-g.z)) * u.z, __fdividef(g.w, 1.0f + __expf(-g.w)) * u.w);
+}
+
+template <int kTokens, bool kGate>
+__global__ void __launch_bounds__(EX<kTokens>::THREADS, 1)
+    experts_product_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
+                           const int *__restrict__ n_tiles, const TokenTile *__restrict__ tiles,
+                           const int *__restrict__ token, int K, int cols, void *__restrict__ out, uint32_t *err) {
+  using X = EX<kTokens>;
+  constexpr int STAGES = X::STAGES, BK = X::BK;
+  constexpr int COLS = kGate ? 64 : 128;  // columns of the output per CTA
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t *smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const bool leader = rank == 0;
+  const uint32_t bar0 = smem_addr(smem + X::OFF_BAR);
+  auto full = [&](int s) { return bar0 + 8u * s; };
+  auto empty = [&](int s) { return bar0 + 8u * (STAGES + s); };
+  auto tfull = [&](int a) { return bar0 + 8u * (2 * STAGES + a); };
+  auto tempty = [&](int a) { return bar0 + 8u * (2 * STAGES + 2 + a); };
+  const uint32_t done_bar = bar0 + 8u * (2 * STAGES + 4);
+  uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(smem + X::OFF_BAR + X::N_BARS * 8);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(full(s), 1);   // the even CTA's expect-tx for both CTAs' loads
+      mbar_init(empty(s), 1);  // the even CTA's commit, to both
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(tfull(a), 1);
+      mbar_init(tempty(a), 2 * X::EPI_WARPS);  // the epilogue warps of both CTAs (even CTA's barrier)
+    }
+    mbar_init(done_bar, 1);
+    mbar_fence_init();
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(smem_addr(tmem_holder), X::TMEM_COLS);
+    tmem_relinquish_pair();
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&wmap);
+    tma_prefetch_desc(&xmap);
+  }
+  tc_fence_before();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_holder;
+
+  const int n_ct = (cols + 2 * COLS - 1) / (2 * COLS);  // column tiles
+  const int64_t total = (int64_t)*n_tiles * n_ct;
+  const int KB = (K + BK - 1) / BK;
+  const int64_t step = gridDim.x >> 1;
+  // consecutive pairs take the column tiles of one token tile (its rows stay in L2)
+  auto tile_at = [&](int64_t t) { return tiles[t / n_ct]; };
+
+  if (warp == 0) {
+    // ------------------------------------------------ TMA: this CTA's weight boxes and token rows
+    int stage = 0;
+    uint32_t phase = 0, pending = 0, pending_phase = 0;
+    bool ok = true;
+    for (int64_t t = blockIdx.x >> 1; ok && t < total; t += step) {
+      const TokenTile tt = tile_at(t);
+      const int col = (int)(t % n_ct) * 2 * COLS + (int)rank * COLS;
+      const int half = tt.width / 2;  // token rows of this CTA, a multiple of 8
+      // lane g gathers rows 4 g .. 4 g + 3 of the half; rows past the tile repeat its last one
+      int r[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        int q = (int)rank * half + 4 * lane + i;
+        q = tt.row0 + (q < tt.rows ? q : tt.rows - 1);
+        r[i] = kGate ? token[q] : q;
+      }
+      const uint32_t bytes = 2u * (X::A_STAGE + (uint32_t)half * 128u);
+      for (int kb = 0; kb < KB; ++kb) {
+        if (!__all_sync(kAll, mbar_wait(empty(stage), phase ^ 1u, err))) { ok = false; break; }
+        if (leader && lane == 0) mbar_arrive_expect_tx(full(stage), bytes);
+        __syncwarp();
+        const uint32_t fb = mapa_shared(full(stage), 0);
+        const uint32_t a_dst = smem_addr(smem + stage * X::A_STAGE);
+        if (lane < 2)  // kGate: the gate's box, then the up box `cols` further on
+          tma_load_3d_pair(a_dst + lane * X::BOX, &wmap, col + lane * (kGate ? cols : 64), kb * BK, tt.expert, fb);
+        if (4 * lane < half)
+          tma_gather4_pair(smem_addr(smem + X::OFF_B + stage * X::B_STAGE) + lane * 512, &xmap, kb * BK, r[0], r[1], r[2],
+                           r[3], fb);
+        pending |= 1u << stage;
+        pending_phase = (pending_phase & ~(1u << stage)) | (phase << stage);
+        if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+      }
+    }
+    // the even CTA's barriers count every load; it waits for the last ones before leaving
+    if (leader)
+      for (int s = 0; s < STAGES; ++s)
+        if (pending & (1u << s)) mbar_wait(full(s), (pending_phase >> s) & 1u, err);
+  } else if (warp == 1) {
+    // ------------------------------------------------ MMA issuer (even CTA)
+    if (leader && lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0, i = 0;
+      bool ok = true;
+      for (int64_t t = blockIdx.x >> 1; ok && t < total; t += step, ++i) {
+        const uint32_t acc = i & 1u, use = i >> 1;
+        const uint32_t idesc = idesc_bf16_f32(256, (uint32_t)tile_at(t).width, 0, 1);
+        if (!mbar_wait(tempty(acc), (use & 1u) ^ 1u, err)) break;
+        tc_fence_after();
+        const uint32_t d = tmem_base + acc * X::ACC_STRIDE;
+        for (int kb = 0; kb < KB; ++kb) {
+          if (!mbar_wait(full(stage), phase, err)) { ok = false; break; }
+          tc_fence_after();
+          const uint32_t a0 = smem_addr(smem + stage * X::A_STAGE);
+          const uint32_t b0 = smem_addr(smem + X::OFF_B + stage * X::B_STAGE);
+#pragma unroll
+          for (int k = 0; k < BK / 16; ++k) {
+            // weights: MN-major, 64-column boxes BOX apart, 8 K-rows 1024 B apart, 16 (2 KB) per step
+            const uint64_t adesc = smem_desc(a0 + 2048u * k, (uint32_t)X::BOX, 1024u, kSwizzle128B);
+            // tokens: K-major, 8-row groups 1024 B apart, 32 B per step
+            const uint64_t bdesc = smem_desc(b0 + 32u * k, 16u, 1024u, kSwizzle128B);
+            tc_mma_f16_pair(d, adesc, bdesc, idesc, (kb | k) != 0 ? 1u : 0u);
+          }
+          tc_commit_pair_both(empty(stage), 3);
+          if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+        }
+        if (!ok) break;
+        tc_commit_pair_both(tfull(acc), 3);
+      }
+      tc_commit_pair(done_bar);
+      mbar_wait(done_bar, 0, err);
+    }
+  } else {
+    // ------------------------------------------------ epilogue: lane = one M row (weight column)
+    const int quad = warp & 3, et = threadIdx.x - 64;
+    float *stg = reinterpret_cast<float *>(smem + X::OFF_STG);
+    uint32_t i = 0, n_chunk = 0;
+    bool ok = true;
+    for (int64_t t = blockIdx.x >> 1; t < total; t += step, ++i) {
+      const uint32_t acc = i & 1u, use = i >> 1;
+      const TokenTile tt = tile_at(t);
+      const int col = (int)(t % n_ct) * 2 * COLS + (int)rank * COLS;
+      ok = group_and<1, 32 * X::EPI_WARPS>(ok && mbar_wait(tfull(acc), use & 1u, err));
+      tc_fence_after();
+      const uint32_t tb = tmem_base + ((uint32_t)(32 * quad) << 16) + acc * X::ACC_STRIDE;
+      for (int c = 0; ok && c < tt.width; c += X::STG_TOKENS, ++n_chunk) {
+        // 32 tokens (16 where the tile ends) of this lane's column into the staging rows
+        const bool wide = tt.width - c >= 32;
+        uint32_t v[2][16];
+        tmem_ld16(tb + c, v[0]);
+        if (wide) tmem_ld16(tb + c + 16, v[1]);
+        tmem_wait_ld();
+        float *buf = stg + (n_chunk & 1u) * (X::STG / 4);
+        const int m = 32 * quad + lane;
+#pragma unroll
+        for (int k = 0; k < 16; ++k) buf[k * 128 + m] = __uint_as_float(v[0][k]);
+        if (wide) {
+#pragma unroll
+          for (int k = 0; k < 16; ++k) buf[(16 + k) * 128 + m] = __uint_as_float(v[1][k]);
+        }
+        // one barrier per chunk: the buffer of two chunks ago was read before the last barrier
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+        const int n_tok = tt.rows - c < 32 ? tt.rows - c : 32;
+        if (kGate) {
+          __nv_bfloat16 *h = static_cast<__nv_bfloat16 *>(out);
+          const int q = et & 15;  // 4 columns, a token per 16 threads
+          if (col + 4 * q < cols) {
+            for (int k = et >> 4; k < n_tok; k += 8) {
+              const float4 g = *reinterpret_cast<const float4 *>(buf + k * 128 + 4 * q);
+              const float4 u = *reinterpret_cast<const float4 *>(buf + k * 128 + 64 + 4 * q);
+              const float4 y = silu_times(g, u);
+              *reinterpret_cast<uint2 *>(h + (int64_t)(tt.row0 + c + k) * cols + col + 4 * q) =
+                  make_uint2(pack_bf16(y.x, y.y), pack_bf16(y.z, y.w));
+            }
+          }
+        } else {
+          float *y = static_cast<float *>(out);
+          const int q = et & 31;  // 4 columns, a token per warp
+          if (col + 4 * q < cols) {
+            for (int k = et >> 5; k < n_tok; k += 4)
+              *reinterpret_cast<float4 *>(y + (int64_t)(tt.row0 + c + k) * cols + col + 4 * q) =
+                  *reinterpret_cast<const float4 *>(buf + k * 128 + 4 * q);
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_remote(mapa_shared(tempty(acc), 0));
+    }
+  }
+
+  tc_fence_before();
+  cluster_sync();  // every MMA into either CTA's TMEM has completed (the even CTA waited above)
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem_base, X::TMEM_COLS);
+  }
+}
+
+// ---------------------------------------------------------------- the tokens' weighted sums
+//
+// Reads each chosen slot's fp32 row once: HBM bound (or L2, where the rows still lie there).
+__global__ void __launch_bounds__(256) experts_sum_kernel(const float *__restrict__ y, const int *__restrict__ row,
+                                                          const float *__restrict__ weights, int64_t n_tokens, int slots,
+                                                          int dim, __nv_bfloat16 *__restrict__ out) {
+  const int pieces = dim / 8;
+  const int64_t total = n_tokens * pieces;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+    const int64_t t = i / pieces;
+    const int p = (int)(i - t * pieces);
+    float acc[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+    for (int j = 0; j < slots; ++j) {
+      const int r = row[t * slots + j];
+      if (r < 0) continue;
+      const float w = weights[t * slots + j];
+      const float4 *src = reinterpret_cast<const float4 *>(y + (int64_t)r * dim + 8 * p);
+      const float4 a = src[0], b = src[1];
+      acc[0] = fmaf(w, a.x, acc[0]); acc[1] = fmaf(w, a.y, acc[1]);
+      acc[2] = fmaf(w, a.z, acc[2]); acc[3] = fmaf(w, a.w, acc[3]);
+      acc[4] = fmaf(w, b.x, acc[4]); acc[5] = fmaf(w, b.y, acc[5]);
+      acc[6] = fmaf(w, b.z, acc[6]); acc[7] = fmaf(w, b.w, acc[7]);
+    }
+    *reinterpret_cast<uint4 *>(out + t * dim + 8 * p) = make_uint4(
+        pack_bf16(acc[0], acc[1]), pack_bf16(acc[2], acc[3]), pack_bf16(acc[4], acc[5]), pack_bf16(acc[6], acc[7]));
+  }
+}
+
+// ---------------------------------------------------------------- host
+
+size_t r256(size_t x) { return (x + 255) / 256 * 256; }
+
+constexpr int kMinTile = 32;  // the narrowest token tile of the product kernels
+
+struct Layout {
+  size_t n_tiles, tiles, token, row, h, y, total;
+};
+Layout layout(int64_t n_tokens, int slots, const dmel_expert_weights &w) {
+  const size_t n = (size_t)n_tokens * slots;
+  // one tile per started kMinTile tokens of an expert
+  const size_t tiles = n / kMinTile + (n < (size_t)w.n_experts ? n : (size_t)w.n_experts);
+  Layout L;
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t here = at;
+    at += r256(bytes);
+    return here;
+  };
+  L.n_tiles = take(4);
+  L.tiles = take(tiles * sizeof(TokenTile));
+  L.token = take(n * 4);
+  L.row = take(n * 4);
+  L.h = take(n * w.hidden * 2);
+  L.y = take(n * w.dim * 4);
+  L.total = at;
+  return L;
+}
+
+// An expert weight stack [E][K][N] (N contiguous) in boxes of 64 columns x 64 K.
+bool weight_map(CUtensorMap *map, EncodeTiledFn enc, const void *base, int E, int K, int64_t N) {
+  const cuuint64_t dims[3] = {(cuuint64_t)N, (cuuint64_t)K, (cuuint64_t)E};
+  const cuuint64_t strides[2] = {(cuuint64_t)N * 2, (cuuint64_t)N * K * 2};
+  const cuuint32_t box[3] = {64, 64, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Rows [R][K] (K contiguous) for gathering: a box is 64 values of one row.
+bool row_map(CUtensorMap *map, EncodeTiledFn enc, const void *base, int64_t R, int K) {
+  const cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)R};
+  const cuuint64_t strides[1] = {(cuuint64_t)K * 2};
+  const cuuint32_t box[2] = {64, 1};
+  const cuuint32_t estr[2] = {1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int kTokens, bool kGate>
+cudaError_t launch_product(const CUtensorMap &wmap, const CUtensorMap &xmap, const int *n_tiles,
+                           const TokenTile *tiles, const int *token, int K, int cols, void *out, int64_t max_tiles,
+                           uint32_t *err, int num_sms, cudaStream_t stream) {
+  using X = EX<kTokens>;
+  static std::atomic<bool> attr[256];
+  const cudaError_t e = set_smem_attr_once(experts_product_kernel<kTokens, kGate>, X::SMEM_BYTES, attr);
+  if (e != cudaSuccess) return e;
+  const int per_pair = kGate ? 128 : 256;
+  const int64_t work = max_tiles * ((cols + per_pair - 1) / per_pair), pairs = num_sms / 2 > 0 ? num_sms / 2 : 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(2 * (work < pairs ? work : pairs)));
+  cfg.blockDim = dim3(X::THREADS);
+  cfg.dynamicSmemBytes = X::SMEM_BYTES;
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = 2;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, experts_product_kernel<kTokens, kGate>, wmap, xmap, n_tiles, tiles, token, K, cols,
+                            out, err);
+}
+
+}  // namespace
+
+size_t experts_workspace_bytes(int64_t n_tokens, int slots, const dmel_expert_weights &w) {
+  return layout(n_tokens, slots, w).total;
+}
+
+cudaError_t launch_experts(const void *x, int64_t n_tokens, const int32_t *ids, const float *weights, int slots,
+                           const dmel_expert_weights &w, void *out, void *workspace, uint32_t *err, int num_sms,
+                           cudaStream_t stream, int *launches) {
+  EncodeTiledFn enc = encode_tiled_fn();
+  if (!enc) return cudaErrorNotSupported;
+  const Layout L = layout(n_tokens, slots, w);
+  uint8_t *base = static_cast<uint8_t *>(workspace);
+  const int n_slots = (int)(n_tokens * slots);
+  PlanOut plan;
+  plan.n_tiles = reinterpret_cast<int *>(base + L.n_tiles);
+  plan.tiles = reinterpret_cast<TokenTile *>(base + L.tiles);
+  plan.token = reinterpret_cast<int *>(base + L.token);
+  plan.row = reinterpret_cast<int *>(base + L.row);
+  CUtensorMap in_w, in_x, out_w, out_h;
+  if (!weight_map(&in_w, enc, w.w_in, w.n_experts, w.dim, 2 * (int64_t)w.hidden) ||
+      !row_map(&in_x, enc, x, n_tokens, w.dim) || !weight_map(&out_w, enc, w.w_out, w.n_experts, w.hidden, w.dim) ||
+      !row_map(&out_h, enc, base + L.h, n_slots, w.hidden))
+    return cudaErrorInvalidValue;
+  const bool few = n_slots <= 16 * (int64_t)w.n_experts;
+  const int tile_tokens = few ? 32 : 256;
+  const int64_t max_tiles = n_slots / tile_tokens + (n_slots < w.n_experts ? n_slots : w.n_experts);
+  static std::atomic<bool> attr[256];
+  cudaError_t e = set_smem_attr_once(experts_plan_kernel, 33 * 1024 * 4, attr);
+  if (e != cudaSuccess) return e;
+  experts_plan_kernel<<<1, kPlanThreads, (size_t)33 * w.n_experts * 4, stream>>>(ids, n_slots, slots, w.n_experts,
+                                                                                 tile_tokens, plan, err);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  ++*launches;
+  void *h = base + L.h, *y = base + L.y;
+  auto products = [&](auto in, auto down) {
+    cudaError_t s = in(in_w, in_x, plan.n_tiles, plan.tiles, plan.token, w.dim, w.hidden, h, max_tiles, err, num_sms, stream);
+    if (s != cudaSuccess) return s;
+    ++*launches;
+    s = down(out_w, out_h, plan.n_tiles, plan.tiles, plan.token, w.hidden, w.dim, y, max_tiles, err, num_sms, stream);
+    if (s == cudaSuccess) ++*launches;
+    return s;
+  };
+  e = few ? products(launch_product<32, true>, launch_product<32, false>)
+          : products(launch_product<256, true>, launch_product<256, false>);
+  if (e != cudaSuccess) return e;
+  const int64_t blocks = (n_tokens * (w.dim / 8) + 255) / 256, cap = (int64_t)num_sms * 32;
+  experts_sum_kernel<<<(unsigned)(blocks < cap ? blocks : cap), 256, 0, stream>>>(
+      static_cast<const float *>(y), plan.row, weights, n_tokens, slots, w.dim, static_cast<__nv_bfloat16 *>(out));
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  ++*launches;
+  return cudaSuccess;
+}
+
+}  // namespace dmel

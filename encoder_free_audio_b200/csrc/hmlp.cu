@@ -184,34 +184,7 @@ static_assert(B_STAGE % 1024 == 0 && A_KB % 1024 == 0 && OFF_B % 1024 == 0, "swi
 
 __device__ __forceinline__ void epi_bar() { asm volatile("bar.sync 1, %0;" ::"n"(s1::EPI_THREADS) : "memory"); }
 
-// Barrier of a named group that also ANDs a flag across it, so the whole group takes the same
-// branch after a bounded wait.
-template <int kId, int kCount>
-__device__ __forceinline__ bool group_and(bool v) {
-  uint32_t out;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.u32 p, %1, 0;\n\t"
-      "bar.red.and.pred q, %2, %3, p;\n\t"
-      "selp.u32 %0, 1, 0, q;\n\t}\n"
-      : "=r"(out)
-      : "r"((uint32_t)v), "n"(kId), "n"(kCount)
-      : "memory");
-  return out != 0;
-}
-
 __device__ __forceinline__ void gather_bar() { asm volatile("bar.sync 2, 128;" ::: "memory"); }
-
-__device__ __forceinline__ float4 lds4(uint32_t addr) {
-  float4 v;
-  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
-  return v;
-}
-
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<uint32_t *>(&v);
-}
 
 // TMA bulk tensor store of a 2D box from shared memory (no multicast), and its bulk-group
 // bookkeeping: commit, wait until the source may be overwritten (.read) or until done.

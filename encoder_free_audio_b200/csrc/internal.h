@@ -92,6 +92,22 @@ size_t hmlp_workspace_bytes(int64_t n_patches, const dmel_hmlp_weights &w);
 cudaError_t launch_hmlp(const void *images, int n, int H, int W, const dmel_hmlp_weights &w, void *out,
                         void *workspace, uint32_t *err, int num_sms, cudaStream_t stream, int *launches);
 
+// Residual addition + RMSNorm of n_rows rows (arguments checked; out_dtype DMEL_E4M3 writes scales).
+cudaError_t launch_add_rmsnorm(const void *x, const void *residual, int64_t n_rows, int dim, dmel_dtype dtype,
+                               const void *w, float eps, void *residual_out, void *out, dmel_dtype out_dtype,
+                               float *scales, int scale_block, int num_sms, cudaStream_t stream, int *launches);
+
+// Router (arguments checked).
+cudaError_t launch_route(const void *logits, int64_t n_tokens, dmel_dtype dtype, const float *bias,
+                         const dmel_router &r, int32_t *ids, float *weights, int num_sms, cudaStream_t stream,
+                         int *launches);
+
+// Experts' products: workspace bytes and the launch (arguments checked).
+size_t experts_workspace_bytes(int64_t n_tokens, int slots, const dmel_expert_weights &w);
+cudaError_t launch_experts(const void *x, int64_t n_tokens, const int32_t *ids, const float *weights, int slots,
+                           const dmel_expert_weights &w, void *out, void *workspace, uint32_t *err, int num_sms,
+                           cudaStream_t stream, int *launches);
+
 // Raises a kernel's dynamic shared-memory limit to `bytes` once per device. `done` is that
 // kernel's own flag array [256] (by device ordinal); concurrent first calls from several host
 // threads may both set the attribute, which is harmless.

@@ -8,6 +8,7 @@ importing this module without it raises, so nothing can silently fall back to an
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import numpy as np
@@ -22,13 +23,17 @@ DMEL_ERR_CUDA = 3
 DMEL_ERR_TOO_LARGE = 4
 DMEL_F32 = 0
 DMEL_BF16 = 1
+DMEL_E4M3 = 2
 DMEL_DEVERR_CODE_RANGE = 0x1
 DMEL_DEVERR_WAIT_TIMEOUT = 0x2
 DMEL_DEVERR_OFFSETS = 0x4
 DMEL_DEVERR_OUT_ROW = 0x8
+DMEL_DEVERR_EXPERT = 0x10
 DMEL_QUANT_FLOOR = 0
 DMEL_QUANT_ROUND = 1
 DMEL_QUANT_MULAW = 2
+DMEL_ROUTE_SOFTMAX = 0
+DMEL_ROUTE_SIGMOID = 1
 
 
 class Quantizer(ctypes.Structure):
@@ -95,6 +100,14 @@ def _lib():
         L.dmel_hmlp.restype = i32
         L.dmel_shortconv.argtypes = [vp, vp, i32, i64, i32, vp, vp, vp, vp, i32, vp]
         L.dmel_shortconv.restype = i32
+        L.dmel_add_rmsnorm.argtypes = [vp, vp, i64, i32, i32, vp, ctypes.c_float, vp, vp, i32, vp, i32, vp]
+        L.dmel_add_rmsnorm.restype = i32
+        L.dmel_route.argtypes = [vp, i64, i32, vp, ctypes.POINTER(Router), vp, vp, vp]
+        L.dmel_route.restype = i32
+        L.dmel_experts_workspace_size.argtypes = [i64, i32, ctypes.POINTER(ExpertWeights)]
+        L.dmel_experts_workspace_size.restype = sz
+        L.dmel_experts.argtypes = [vp, i64, vp, vp, i32, ctypes.POINTER(ExpertWeights), vp, vp, sz, vp]
+        L.dmel_experts.restype = i32
         L.dmel_embed_noalloc.argtypes = [vp, i64, vp, i32, i32, vp, ctypes.c_float, vp, i32, vp]
         L.dmel_embed_noalloc.restype = i32
         L.dmel_get_device_error.argtypes = [ctypes.POINTER(ctypes.c_uint32), i32]
@@ -361,6 +374,119 @@ def dmel_shortconv(x, seq_offsets, weights, y, state=None, state_out=None, strea
     rc = _lib().dmel_shortconv(_ptr(x), _ptr(seq_offsets), n_seq, int(x.shape[0]), int(x.shape[1]), _ptr(weights),
                                _ptr(state), _ptr(state_out), _ptr(y), _dtype_code(x), _stream(stream))
     _check(rc, "dmel_shortconv")
+
+
+# The decoder-block calls check what C cannot see of a tensor: its device, type and shape, and that
+# it has no gaps. They run on the tensors' device, whichever device is current.
+
+class Router(ctypes.Structure):
+    """dmel_router: sizes, scoring and weighting of dmel_route."""
+    _fields_ = [(k, ctypes.c_int) for k in ("n_experts", "n_shared", "top_k", "n_groups", "topk_groups", "scoring",
+                                            "renormalise")] + [("scale", ctypes.c_float)]
+
+
+class ExpertWeights(ctypes.Structure):
+    """dmel_expert_weights: sizes and device pointers of the experts."""
+    _fields_ = [(k, ctypes.c_int) for k in ("n_experts", "dim", "hidden")] + \
+               [(k, ctypes.c_void_p) for k in ("w_in", "w_out")]
+
+
+_router = functools.lru_cache(maxsize=64)(Router)  # the argument struct of a router's settings
+
+
+def _refuse(where: str, what: str):
+    raise DmelError(DMEL_ERR_INVALID_ARG, f"{where} ({what})")
+
+
+def _addr(t, where: str, name: str, dtype, shape, device):
+    """The address of tensor t, which must have this type, shape and device and no gaps."""
+    if t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+        _refuse(where, f"{name}: want a contiguous {dtype} tensor {tuple(shape)} on {device}, got {t.dtype} "
+                       f"{tuple(t.shape)} on {t.device} with strides {tuple(t.stride())}")
+    return t.data_ptr()
+
+
+def _run_on(device, stream, where: str, entry, *args):
+    """entry(*args, stream) on `device`: on the given stream, or on the device's current one."""
+    import torch
+    if device.type != "cuda":
+        _refuse(where, f"tensors on {device}, want a CUDA device")
+    if stream is not None and stream.device != device:
+        _refuse(where, f"a stream of {stream.device} for tensors on {device}")
+    if device.index == torch.cuda.current_device():
+        raw = torch.cuda.current_stream(device).cuda_stream if stream is None else stream.cuda_stream
+        rc = entry(*args, raw)
+    else:
+        with torch.cuda.device(device):
+            raw = torch.cuda.current_stream(device).cuda_stream if stream is None else stream.cuda_stream
+            rc = entry(*args, raw)
+    if rc != DMEL_OK:
+        raise DmelError(rc, where)
+
+
+def dmel_add_rmsnorm(x, rms_weight, out, residual=None, residual_out=None, eps: float = 1e-6, scales=None,
+                     scale_block: int = 0, stream=None):
+    """dmel_add_rmsnorm on torch CUDA tensors: x [n, D] (fp32 or bf16), rms_weight [D], residual and
+    residual_out [n, D] in x's dtype or None, out [n, D] fp32, bf16 or float8_e4m3fn; for e4m3,
+    scales fp32 [n, ceil(D / scale_block)] ([n, 1] or [n] for scale_block 0, one scale per row)."""
+    import torch
+    where = "dmel_add_rmsnorm"
+    if x.dim() != 2:
+        _refuse(where, f"x: want [rows, dim], got {tuple(x.shape)}")
+    shape, dt, dev = x.shape, x.dtype, x.device
+    n, d = shape
+    odt = DMEL_E4M3 if out.dtype is torch.float8_e4m3fn else _dtype_code(out)
+    sc = None
+    if scales is not None:
+        blocks = -(-d // scale_block) if scale_block > 0 else 1
+        sc = _addr(scales, where, "scales", torch.float32, (n,) if scales.dim() == 1 and blocks == 1 else (n, blocks), dev)
+    _run_on(dev, stream, where, _lib().dmel_add_rmsnorm, _addr(x, where, "x", dt, shape, dev),
+            None if residual is None else _addr(residual, where, "residual", dt, shape, dev), n, d, _dtype_code(x),
+            _addr(rms_weight, where, "rms_weight", dt, (d,), dev), eps,
+            None if residual_out is None else _addr(residual_out, where, "residual_out", dt, shape, dev),
+            _addr(out, where, "out", out.dtype, shape, dev), odt, sc, scale_block)
+
+
+def dmel_route(logits, ids, weights, n_shared: int = 0, bias=None, scoring: int = DMEL_ROUTE_SIGMOID, n_groups: int = 1,
+               topk_groups: int = 1, renormalise: bool = True, scale: float = 1.0, stream=None):
+    """dmel_route on torch CUDA tensors: logits [T, n_experts + n_shared] (fp32 or bf16), ids int32 and
+    weights fp32 [T, top_k + n_shared] (their width sets top_k), bias fp32 [n_experts] or None."""
+    import torch
+    where = "dmel_route"
+    if logits.dim() != 2 or ids.dim() != 2:
+        _refuse(where, f"logits and ids: want two dimensions, got {tuple(logits.shape)} and {tuple(ids.shape)}")
+    dev, n = logits.device, logits.shape[0]
+    e, shape = logits.shape[1] - n_shared, (n, ids.shape[1])
+    r = _router(e, n_shared, shape[1] - n_shared, n_groups, topk_groups, scoring, int(renormalise), scale)
+    _run_on(dev, stream, where, _lib().dmel_route, _addr(logits, where, "logits", logits.dtype, logits.shape, dev), n,
+            _dtype_code(logits), None if bias is None else _addr(bias, where, "bias", torch.float32, (e,), dev), r,
+            _addr(ids, where, "ids", torch.int32, shape, dev), _addr(weights, where, "weights", torch.float32, shape, dev))
+
+
+def dmel_experts_workspace_size(n_tokens: int, slots: int, n_experts: int, dim: int, hidden: int) -> int:
+    """Device workspace bytes of dmel_experts."""
+    return int(_lib().dmel_experts_workspace_size(int(n_tokens), int(slots),
+                                                  ExpertWeights(int(n_experts), int(dim), int(hidden))))
+
+
+def dmel_experts(x, ids, weights, w_in, w_out, out, workspace, stream=None):
+    """dmel_experts on torch CUDA tensors: x and out bf16 [T, D], ids int32 and weights fp32 [T, slots],
+    w_in bf16 [E, D, 2 H] (gate columns, then up columns), w_out bf16 [E, H, D], workspace uint8."""
+    import torch
+    where = "dmel_experts"
+    if x.dim() != 2 or ids.dim() != 2 or w_out.dim() != 3:
+        _refuse(where, f"x, ids and w_out: want 2, 2 and 3 dimensions, got {tuple(x.shape)}, {tuple(ids.shape)} and "
+                       f"{tuple(w_out.shape)}")
+    dev, bf16 = x.device, torch.bfloat16
+    (n, d), (e, h, _), slots = x.shape, w_out.shape, ids.shape[1]
+    w = ExpertWeights(e, d, h, _addr(w_in, where, "w_in", bf16, (e, d, 2 * h), dev),
+                      _addr(w_out, where, "w_out", bf16, (e, h, d), dev))
+    _run_on(dev, stream, where, _lib().dmel_experts, _addr(x, where, "x", bf16, (n, d), dev), n,
+            _addr(ids, where, "ids", torch.int32, (n, slots), dev),
+            _addr(weights, where, "weights", torch.float32, (n, slots), dev), slots, w,
+            _addr(out, where, "out", bf16, (n, d), dev),
+            None if workspace is None else _addr(workspace, where, "workspace", torch.uint8, workspace.shape, dev),
+            0 if workspace is None else workspace.numel())
 
 
 def dmel_splice_plan(sentinel_pos, frame_offsets, seq_len: int):

@@ -57,7 +57,9 @@ typedef enum {
   DMEL_ERR_TOO_LARGE = 4    /* dmel_embed_noalloc: the request needs more than its fixed scratch */
 } dmel_status;
 
-typedef enum { DMEL_F32 = 0, DMEL_BF16 = 1 } dmel_dtype;
+/* DMEL_E4M3 (8 bits: 4 exponent, 3 mantissa, largest value 448, no infinity) is an output type of
+ * dmel_add_rmsnorm only; every other entry point takes DMEL_F32 and DMEL_BF16. */
+typedef enum { DMEL_F32 = 0, DMEL_BF16 = 1, DMEL_E4M3 = 2 } dmel_dtype;
 
 #define DMEL_SAMPLE_RATE 16000
 #define DMEL_HOP 800        /* 50 ms: 20 frames per second */
@@ -73,6 +75,7 @@ typedef enum { DMEL_F32 = 0, DMEL_BF16 = 1 } dmel_dtype;
 #define DMEL_DEVERR_WAIT_TIMEOUT 0x2u /* a pipeline wait inside a kernel gave up (results invalid) */
 #define DMEL_DEVERR_OFFSETS 0x4u     /* device frame offsets disagree with the sample offsets */
 #define DMEL_DEVERR_OUT_ROW 0x8u     /* an output row index outside [0, out_n_rows) (row not written) */
+#define DMEL_DEVERR_EXPERT 0x10u     /* an expert id outside [-1, n_experts) (its slot adds nothing) */
 
 /* Frames of one clip of n_samples samples: floor(n_samples / 800) (20 per second of audio;
  * "Inside Inkling: Audio Design", Part 1 · Modeling). Host only, pure. Returns -1 for
@@ -330,6 +333,105 @@ dmel_status dmel_forward_rows(const float *wav, const int64_t *sample_offsets, c
 dmel_status dmel_shortconv(const void *x, const int64_t *seq_offsets, int n_seq, int64_t n_tokens, int channels,
                            const float *weights, const void *state, void *state_out, void *y, dmel_dtype dtype,
                            dmel_stream_t stream);
+
+/* ---- The decoder block around the ShortConv ("Inside Inkling: Audio Design", Part 3 · Inference:
+ * the ShortConv on the residual-branch outputs, a sigmoid router over 256 routed and 2 shared
+ * experts with 6 chosen per token and a joint normalisation of the chosen and the shared ones).
+ * The three calls follow one another: a branch's output joins the residual stream and is normed,
+ * the router's logits of the normed rows become each token's experts and weights, and the
+ * experts' products give the next branch output. Each runs prompts and single tokens alike. */
+
+/* Residual addition and RMSNorm of n_rows rows of dim values:
+ *     s = x + residual,   residual_out = s,   y = rms_weight * s / sqrt(mean(s^2) + eps)
+ * x             [n_rows x dim] in dtype (fp32 or bf16); this and the arrays in dtype below: device,
+ *               16-byte aligned
+ * residual      NULL (s = x) or [n_rows x dim] in dtype
+ * rms_weight    [dim] in dtype
+ * eps           > 0
+ * residual_out  NULL or [n_rows x dim] in dtype: s rounded to dtype
+ * out           [n_rows x dim] in out_dtype: DMEL_F32, DMEL_BF16 (16-byte aligned) or DMEL_E4M3 (8-byte)
+ * scales        NULL unless out_dtype is DMEL_E4M3; then fp32 [n_rows x ceil(dim / scale_block)],
+ *               or [n_rows] for scale_block 0, 4-byte aligned
+ * scale_block   consecutive columns that share a scale: 32, 64, 128, or 0 for the whole row (the
+ *               last block of a row may be shorter); 0 for the other output types
+ * dim           a positive multiple of 8, at most 16384
+ * The sum, its square mean and y are fp32 and y comes from the unrounded sum; residual_out and out
+ * round once, to nearest even. For DMEL_E4M3 a block's scale is max(largest |y|, 1e-30) / 448 and
+ * out holds e4m3(y / scale), so out * scale is y within e4m3's rounding; a NaN in y is NaN in out
+ * and does not enter the scale. Squares above fp32's range overflow as they do in the formula.
+ * residual_out may be x or residual, and out may be x or residual when out_dtype is dtype;
+ * otherwise the outputs must not overlap the inputs or one another (DMEL_ERR_INVALID_ARG).
+ * Asynchronous on stream, one launch. */
+dmel_status dmel_add_rmsnorm(const void *x, const void *residual, int64_t n_rows, int dim, dmel_dtype dtype,
+                             const void *rms_weight, float eps, void *residual_out, void *out, dmel_dtype out_dtype,
+                             float *scales, int scale_block, dmel_stream_t stream);
+
+/* Routing of tokens to experts. Per token, with logits l over n_experts routed experts and then
+ * n_shared shared ones:
+ *   scores   sigmoid: s_e = 1 / (1 + exp(-l_e)); softmax: s = softmax of all the token's logits
+ *   choice   c_e = s_e + bias_e over the routed experts (bias NULL: their order is the logits')
+ *   groups   n_groups > 1: groups of n_experts / n_groups consecutive experts are rated by the sum
+ *            of their two largest c (one, where only one is there); experts outside the
+ *            topk_groups best groups are not chosen
+ *   chosen   the top_k largest c in descending order, then every shared expert, ids
+ *            n_experts .. n_experts + n_shared - 1; equal values go to the lower index, for
+ *            experts and for groups
+ *   weights  s of the chosen (without the bias), divided by their sum when renormalise is not 0,
+ *            times scale
+ * The choice is made as 64-bit arithmetic makes it: values that fp32 cannot tell apart are compared
+ * again in fp64. An expert whose logit is -inf or NaN is never chosen; a slot left without an
+ * expert (a masked token, a masked shared expert) has id -1 and weight 0. +inf counts as FLT_MAX.
+ * A NaN in bias counts as -inf there.
+ * logits   [n_tokens x (n_experts + n_shared)] in dtype (fp32 or bf16), device, aligned to dtype
+ * bias     NULL or fp32 [n_experts]
+ * ids      int32 [n_tokens x (top_k + n_shared)]
+ * weights  fp32 [n_tokens x (top_k + n_shared)]
+ * Asynchronous on stream, one launch. */
+typedef enum { DMEL_ROUTE_SOFTMAX = 0, DMEL_ROUTE_SIGMOID = 1 } dmel_route_scoring;
+
+typedef struct {
+  int n_experts;   /* routed experts, 1 .. 1024 */
+  int n_shared;    /* shared experts, >= 0 */
+  int top_k;       /* 1 .. topk_groups * (n_experts / n_groups); top_k + n_shared at most 32 */
+  int n_groups;    /* divides n_experts, 1 .. 32 (1: no groups) */
+  int topk_groups; /* 1 .. n_groups */
+  int scoring;     /* dmel_route_scoring */
+  int renormalise; /* nonzero: the chosen weights sum to scale */
+  float scale;     /* finite */
+} dmel_router;
+
+dmel_status dmel_route(const void *logits, int64_t n_tokens, dmel_dtype dtype, const float *bias, const dmel_router *r,
+                       int32_t *ids, float *weights, dmel_stream_t stream);
+
+/* The experts' gated products, weighted and summed per token:
+ *     out[t] = sum_j weights[t, j] * (silu(x[t] G_e) * (x[t] U_e)) D_e,   e = ids[t, j]
+ * with silu(a) = a / (1 + exp(-a)), [G_e | U_e] = w_in[e] and D_e = w_out[e].
+ * x         bf16 [n_tokens x dim], device, 16-byte aligned
+ * ids       int32 [n_tokens x slots] (dmel_route's): -1 adds nothing; another id outside
+ *           [0, n_experts) adds nothing and sets DMEL_DEVERR_EXPERT; a token may name an expert twice
+ * weights   fp32 [n_tokens x slots]; not read where the id is -1
+ * slots     1 .. 64
+ * out       bf16 [n_tokens x dim] (a token without an expert gets zeros); must not overlap x
+ * workspace device scratch of dmel_experts_workspace_size(...) bytes, 256-byte aligned; calls that
+ *           may run at the same time need one each
+ * Products sum in fp32; the gated hidden row is rounded to bf16 once (the second product's
+ * operand), each expert's output row stays fp32 until the token's sum, which is rounded to bf16.
+ * Results do not depend on how tokens are batched, up to fp32 summation inside the tensor cores.
+ * n_tokens * slots at most 2^30. Asynchronous on stream, four launches. */
+typedef struct {
+  int n_experts;     /* 1 .. 1024 */
+  int dim;           /* model width, a positive multiple of 8, at most 65536 */
+  int hidden;        /* an expert's hidden width, likewise */
+  const void *w_in;  /* bf16 [n_experts x dim x 2 hidden] row-major: the gate's columns, then the up columns */
+  const void *w_out; /* bf16 [n_experts x hidden x dim] row-major */
+} dmel_expert_weights; /* device pointers, 16-byte aligned */
+
+/* Bytes of device workspace dmel_experts needs (0 for no tokens or sizes out of contract; the
+ * weight pointers are not looked at). */
+size_t dmel_experts_workspace_size(int64_t n_tokens, int slots, const dmel_expert_weights *w);
+dmel_status dmel_experts(const void *x, int64_t n_tokens, const int32_t *ids, const float *weights, int slots,
+                         const dmel_expert_weights *w, void *out, void *workspace, size_t workspace_bytes,
+                         dmel_stream_t stream);
 
 /* ---- hMLP patchifier (vision; "Inside Inkling: Audio Design", Part 1 · Modeling: a 4-layer
  * hMLP over 40x40 patches; "Why Thinking Machines Built Inkling Without a Vision Encoder":

@@ -338,6 +338,101 @@ def shortconv(x: np.ndarray, seq_offsets, w: np.ndarray, state: np.ndarray | Non
     return y, so
 
 
+# ---------------------------------------------------------------- the decoder block around ShortConv
+
+E4M3_MAX = 448.0
+
+
+def add_rmsnorm(x: np.ndarray, residual, w: np.ndarray, eps: float, scale_block: int | None = None):
+    """Residual addition and RMSNorm in fp64: (s, y) with s = x + residual and
+    y = w s / sqrt(mean(s^2) + eps) per row; with scale_block (0: the row) also the scales
+    max(largest |y| of the block, 1e-30) / 448, as (s, y, scales)."""
+    s = np.asarray(x, np.float64) + (0.0 if residual is None else np.asarray(residual, np.float64))
+    y = np.zeros_like(s)
+    for i in range(s.shape[0]):
+        y[i] = w * s[i] / np.sqrt(np.sum(s[i] * s[i]) / s.shape[1] + eps)
+    if scale_block is None:
+        return s, y
+    step = scale_block or s.shape[1]
+    cols = range(0, s.shape[1], step)
+    scales = np.array([[max(np.abs(y[i, c:c + step]).max(), 1e-30) / E4M3_MAX for c in cols] for i in range(s.shape[0])])
+    return s, y, scales.reshape(s.shape[0], len(cols))
+
+
+def route(logits: np.ndarray, n_shared: int, top_k: int, sigmoid: bool, bias=None, n_groups: int = 1,
+          topk_groups: int = 1, renormalise: bool = True, scale: float = 1.0):
+    """Routing in fp64, token by token: (ids [T, top_k + n_shared], weights). Experts are ordered by
+    score plus bias (by the logits themselves without a bias), equal ones by index; -inf and NaN
+    logits are never chosen; an empty slot is (-1, 0)."""
+    logits = np.asarray(logits, np.float64)
+    T, E = logits.shape[0], logits.shape[1] - n_shared
+    ids = np.full((T, top_k + n_shared), -1, np.int64)
+    weights = np.zeros((T, top_k + n_shared))
+    for t in range(T):
+        l = np.where(np.isnan(logits[t]), -np.inf, np.minimum(logits[t], float(np.finfo(np.float32).max)))
+        with np.errstate(over="ignore"):
+            if sigmoid:
+                s = 1.0 / (1.0 + np.exp(-l))
+            elif np.isinf(l).all():
+                s = np.zeros_like(l)
+            else:
+                s = np.exp(l - l.max())
+                s = s / s.sum()
+        c = s[:E] + (0.0 if bias is None else np.asarray(bias, np.float64))
+        alive = [e for e in range(E) if l[e] > -np.inf and c[e] > -np.inf]
+        if n_groups > 1:
+            per = E // n_groups
+            rated = []
+            for g in range(n_groups):
+                two = sorted((c[e] for e in alive if e // per == g), reverse=True)[:2]
+                rated.append(sum(two) if two else -np.inf)
+            kept = set(sorted(range(n_groups), key=lambda g: (-rated[g], g))[:topk_groups])
+            alive = [e for e in alive if e // per in kept]
+        order = sorted(alive, key=lambda e: (-(l[e] if bias is None else c[e]), e))[:top_k]
+        chosen = [(j, e) for j, e in enumerate(order)]
+        chosen += [(top_k + i, E + i) for i in range(n_shared) if l[E + i] > -np.inf]
+        if not chosen:
+            continue
+        ln = np.array([l[e] for _, e in chosen])
+        w = np.array([s[e] for _, e in chosen])
+        if renormalise:
+            # log of the scores up to a constant, so that tiny ones keep their ratios
+            ls = -np.logaddexp(0.0, -ln) if sigmoid else ln
+            w = np.exp(ls - ls.max())
+            w = w / w.sum()
+        for (j, e), v in zip(chosen, w):
+            ids[t, j], weights[t, j] = e, v * scale
+    return ids, weights
+
+
+def experts(x: np.ndarray, ids: np.ndarray, weights: np.ndarray, w_in: np.ndarray, w_out: np.ndarray):
+    """The experts' products in fp64, slot by slot: out[t] = sum_j weights[t, j] (silu(x G) * (x U)) D of
+    expert ids[t, j]. Returns (out, h [T, slots, H], how far bf16 rounding of h and the fp32 sums (one
+    rounding of 2^-23 per 16 products) may move each output at most)."""
+    x, w_in, w_out = (np.asarray(a, np.float64) for a in (x, w_in, w_out))
+    T, slots = ids.shape
+    H = w_out.shape[1]
+    out = np.zeros((T, w_out.shape[2]))
+    spread = np.zeros_like(out)
+    hidden = np.zeros((T, slots, H))
+    for t in range(T):
+        for j in range(slots):
+            e = ids[t, j]
+            if e < 0 or e >= w_in.shape[0]:
+                continue
+            a = x[t] @ w_in[e]
+            g, u = a[:H], a[H:]
+            h = g / (1.0 + np.exp(-g)) * u
+            b = np.abs(x[t]) @ np.abs(w_in[e])
+            hidden[t, j] = h
+            out[t] += weights[t, j] * (h @ w_out[e])
+            # rounding h moves it by 2^-8 of itself; the fp32 sums of g and u move it by their own
+            sums = (x.shape[1] / 16 + 16) * 2.0 ** -23
+            dh = 2.0 ** -8 * np.abs(h) + sums * (1.1 * b[:H] * np.abs(u) + np.abs(g) * b[H:])
+            spread[t] += abs(weights[t, j]) * ((dh + (H / 16 + 16) * 2.0 ** -23 * np.abs(h)) @ np.abs(w_out[e]))
+    return out, hidden, spread
+
+
 # ---------------------------------------------------------------- hMLP patchifier (vision)
 
 HMLP_PATCH = 40

@@ -1,0 +1,507 @@
+"""The decoder-block operators on the GPU against the fp64 oracle: residual addition with RMSNorm, routing,
+experts, and the three in a row behind the ShortConv."""
+import numpy as np
+import pytest
+import torch
+
+from encoder_free_audio_b200 import build, dmel
+
+pytestmark = pytest.mark.gpu
+
+DEV = torch.device("cuda:0")
+BF16, F32, E4M3 = torch.bfloat16, torch.float32, torch.float8_e4m3fn
+HALF_STEP = {BF16: 2.0 ** -8, F32: 2.0 ** -24}  # a rounding, relative to the value
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    build.build()
+    dmel.library()
+    dmel.dmel_get_device_error(clear=True)
+    yield
+
+
+def f64(t):
+    return t.detach().double().cpu().numpy()
+
+
+# ------------------------------------------------------------------------------ add + RMSNorm
+
+def norm_inputs(seed, n, d, dt, residual=True):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    x = torch.randn((n, d), generator=g, device=DEV)
+    r = torch.randn((n, d), generator=g, device=DEV) * torch.exp(torch.randn((n, 1), generator=g, device=DEV))
+    w = 1.0 + 0.2 * torch.randn(d, generator=g, device=DEV)
+    return x.to(dt), r.to(dt) if residual else None, w.to(dt)
+
+
+def norm_bound(d):
+    """Relative error of fp32 y: the fp32 sum s (1), a chain of at most d / 8 / 32 * 8 squares in a thread
+    and ten additions across threads, halved by the square root; its division, addition, square root and
+    reciprocal (4, of which the square root halves two); two products (2). In units of 2^-24."""
+    return ((d / 32 + 16 + 10) / 2 + 1 + 4 + 2) * 2.0 ** -24
+
+
+@pytest.mark.parametrize("dt", [F32, BF16])
+@pytest.mark.parametrize("odt", [F32, BF16])
+@pytest.mark.parametrize("n,d", [(1, 8), (3, 40), (5, 256), (2, 264), (7, 1000), (4, 6144), (3, 8192), (2, 8200), (2, 16384)])
+def test_add_rmsnorm(dt, odt, n, d, oracle_mod):
+    for residual in (True, False):
+        x, r, w = norm_inputs(d + n, n, d, dt, residual)
+        out, rout = torch.empty((n, d), dtype=odt, device=DEV), torch.empty((n, d), dtype=dt, device=DEV)
+        dmel.dmel_add_rmsnorm(x, w, out, residual=r, residual_out=rout, eps=1e-5)
+        assert dmel.dmel_last_launch_count() == 1
+        s, y = oracle_mod.add_rmsnorm(f64(x), None if r is None else f64(r), f64(w), 1e-5)
+        assert (np.abs(f64(rout) - s) <= (HALF_STEP[dt] * 1.001 + 2.0 ** -24) * np.abs(s)).all()
+        assert (np.abs(f64(out) - y) <= (HALF_STEP[odt] * 1.001 + norm_bound(d)) * np.abs(y) + 1e-37).all()
+        alone = torch.empty_like(out)
+        dmel.dmel_add_rmsnorm(x, w, alone, residual=r, eps=1e-5)  # without the stream out
+        assert torch.equal(alone, out)
+
+
+@pytest.mark.parametrize("dt", [F32, BF16])
+@pytest.mark.parametrize("block", [0, 32, 64, 128])
+@pytest.mark.parametrize("n,d", [(1, 8), (3, 40), (5, 256), (2, 1000), (3, 5992), (4, 6144), (2, 16384)])
+def test_add_rmsnorm_e4m3(dt, block, n, d, oracle_mod):
+    x, r, w = norm_inputs(7 * d + n, n, d, dt)
+    x[:, :8] *= 30.0       # blocks of very different size
+    if d > 200:
+        x[n - 1, 128:192] = 0.0
+        r[n - 1, 128:192] = 0.0  # and whole blocks of zeros
+    blocks = -(-d // block) if block else 1
+    out = torch.empty((n, d), dtype=E4M3, device=DEV)
+    scales, rout = torch.empty((n, blocks), device=DEV), torch.empty_like(x)
+    dmel.dmel_add_rmsnorm(x, w, out, residual=r, residual_out=rout, eps=1e-6, scales=scales, scale_block=block)
+    s, y, sc = oracle_mod.add_rmsnorm(f64(x), f64(r), f64(w), 1e-6, block)
+    b = norm_bound(d)
+    assert (np.abs(f64(scales) - sc) <= (b + 2 * 2.0 ** -24) * sc).all()
+    each = np.repeat(sc, block or d, axis=1)[:, :d]
+    # half a step of e4m3: 2^-4 of the value, 2^-10 below its smallest normal value 2^-6
+    q = f64(out.float())
+    assert np.isfinite(q).all() and (np.abs(q) <= 448).all()
+    assert (np.abs(q - y / each) <= (2.0 ** -4 + 2 * b + 4 * 2.0 ** -24) * np.abs(y / each) + 2.0 ** -10).all()
+    top = np.array([[np.abs(q[i, c:c + (block or d)]).max() for c in range(0, d, block or d)] for i in range(n)])
+    assert ((top == 448) | (sc <= 1e-30)).all()  # each block's largest value fills the range
+    assert (np.abs(f64(rout) - s) <= (HALF_STEP[dt] * 1.001 + 2.0 ** -24) * np.abs(s)).all()
+
+
+def test_add_rmsnorm_zero_rows_nan_and_infinity():
+    d = 520
+    x, r, w = norm_inputs(3, 6, d, F32)
+    x[1] = 0.0; r[1] = 0.0          # a row of zeros: zeros, whatever eps is
+    x[2, 17] = float("nan")         # NaN spreads over its row
+    x[3, 5] = float("inf")          # an infinity: the others are scaled to zero, itself is inf * 0
+    x[4] = 1e-30; r[4] = 0.0        # squares that underflow: eps decides
+    out, y8 = torch.empty_like(x), torch.empty((6, d), dtype=E4M3, device=DEV)
+    sc = torch.empty((6, 5), device=DEV)
+    dmel.dmel_add_rmsnorm(x, w, out, residual=r, eps=1e-6)
+    dmel.dmel_add_rmsnorm(x, w, y8, residual=r, eps=1e-6, scales=sc, scale_block=128)
+    clean, clean8, sc_clean = torch.empty_like(x), torch.empty_like(y8), torch.empty_like(sc)
+    for i in (0, 5):  # the rows around them are as they are alone
+        dmel.dmel_add_rmsnorm(x[i:i + 1], w, clean[i:i + 1], residual=r[i:i + 1], eps=1e-6)
+        dmel.dmel_add_rmsnorm(x[i:i + 1], w, clean8[i:i + 1], residual=r[i:i + 1], eps=1e-6, scales=sc_clean[i:i + 1],
+                              scale_block=128)
+        assert torch.equal(out[i], clean[i]) and torch.equal(y8[i].view(torch.uint8), clean8[i].view(torch.uint8))
+    assert (out[1] == 0).all() and (y8[1].float() == 0).all() and (sc[1] > 0).all()
+    assert out[2].isnan().all() and y8[2].float().isnan().all() and sc[2].isfinite().all()
+    assert out[3, 5].isnan() and (out[3, :5] == 0).all() and (out[3, 6:] == 0).all()
+    torch.testing.assert_close(out[4], 1e-30 / 1e-3 * w, rtol=1e-5, atol=0)
+
+
+@pytest.mark.parametrize("dt", [F32, BF16])
+def test_add_rmsnorm_in_place(dt):
+    """The stream updated in its own buffer and the normed rows over x: the same bits; rows behind the
+    call's stay as they were."""
+    n, d = 9, 6144
+    x, r, w = norm_inputs(11, n, d, dt)
+    out, rout = torch.empty_like(x), torch.empty_like(r)
+    dmel.dmel_add_rmsnorm(x, w, out, residual=r, residual_out=rout)
+    for a, b in (("x", "r"), ("r", "x")):
+        bufs = {"x": x.clone(), "r": r.clone()}
+        dmel.dmel_add_rmsnorm(bufs["x"], w, bufs[a], residual=bufs["r"], residual_out=bufs[b])
+        assert torch.equal(bufs[a], out) and torch.equal(bufs[b], rout)
+    big = torch.full((n + 3, d), 7.0, dtype=dt, device=DEV)
+    dmel.dmel_add_rmsnorm(x, w, big[:n], residual=r)
+    assert torch.equal(big[:n], out) and (big[n:] == 7.0).all()
+
+
+def test_add_rmsnorm_more_rows_than_blocks(oracle_mod):
+    """Rows past the largest grid: every row is its own (narrow rows keep it small)."""
+    n, d = 148 * 64 * 8 + 77, 16
+    x, r, w = norm_inputs(12, n, d, F32)
+    out, scales = torch.empty((n, d), dtype=E4M3, device=DEV), torch.empty(n, device=DEV)
+    dmel.dmel_add_rmsnorm(x, w, out, residual=r, scales=scales)
+    s = x.double() + r.double()
+    y = s * w.double() / torch.sqrt((s * s).mean(1, keepdim=True) + 1e-6)
+    sc = y.abs().amax(1) / 448
+    assert ((scales.double() - sc).abs() <= (norm_bound(d) + 2.0 ** -23) * sc).all()
+    q = y / sc[:, None]
+    assert ((out.double() - q).abs() <= (2.0 ** -4 + 2 * norm_bound(d) + 2.0 ** -22) * q.abs() + 2.0 ** -10).all()
+
+
+# ------------------------------------------------------------------------------ routing
+
+def run_route(logits, k, bias=None, shared=0, **kw):
+    n = logits.shape[0]
+    ids = torch.full((n, k + shared), -7, dtype=torch.int32, device=DEV)
+    wts = torch.full((n, k + shared), 9.0, device=DEV)
+    dmel.dmel_route(logits, ids, wts, n_shared=shared, bias=bias, **kw)
+    return ids.cpu().numpy(), wts.double().cpu().numpy()
+
+
+def check_route(logits, k, oracle_mod, bias=None, shared=0, sigmoid=True, groups=1, topk_groups=1, renorm=True, scale=1.0):
+    ids, w = run_route(logits, k, bias, shared, scoring=int(sigmoid), n_groups=groups, topk_groups=topk_groups,
+                       renormalise=renorm, scale=scale)
+    rid, rw = oracle_mod.route(f64(logits), shared, k, sigmoid, None if bias is None else f64(bias), groups, topk_groups,
+                               renorm, scale)
+    np.testing.assert_array_equal(ids, rid)
+    # two exponentials of rounded differences (their size, at most `spread`, and 4 units each), a sum of up
+    # to 32 (5; 1024 logits in a softmax's denominator: 10), divisions and products, in units of 2^-24
+    l = f64(logits)
+    l = l[np.isfinite(l)]
+    spread = (l.max() - l.min()) if l.size else 0.0
+    assert (np.abs(w - rw) <= (2 * spread + 28) * 2.0 ** -24 * np.abs(rw) + 1e-37).all()
+    return ids, w
+
+
+@pytest.mark.parametrize("dt", [F32, BF16])
+@pytest.mark.parametrize("sigmoid", [True, False])
+@pytest.mark.parametrize("n,e,shared,k", [(1, 1, 0, 1), (1, 256, 2, 6), (5, 7, 0, 7), (33, 60, 1, 4), (130, 256, 0, 8),
+                                          (64, 31, 3, 5), (64, 33, 0, 2), (17, 1024, 0, 32), (9, 513, 4, 12)])
+def test_route(dt, sigmoid, n, e, shared, k, oracle_mod):
+    g = torch.Generator(device=DEV).manual_seed(e + n)
+    logits = (2.0 * torch.randn((n, e + shared), generator=g, device=DEV)).to(dt)
+    bias = 0.1 * torch.randn(e, generator=g, device=DEV)
+    for b in (bias, torch.zeros(e, device=DEV), None):
+        check_route(logits, k, oracle_mod, b, shared, sigmoid)
+    check_route(logits, k, oracle_mod, bias, shared, sigmoid, renorm=False, scale=-2.5)
+
+
+@pytest.mark.parametrize("dt", [F32, BF16])
+@pytest.mark.parametrize("e,groups,topk_groups,k", [(256, 8, 4, 8), (64, 32, 5, 9), (60, 4, 3, 7), (12, 12, 5, 5), (96, 3, 1, 20),
+                                                    (6, 2, 2, 6), (1024, 16, 2, 16), (50, 5, 1, 10)])
+def test_route_groups(dt, e, groups, topk_groups, k, oracle_mod):
+    g = torch.Generator(device=DEV).manual_seed(e)
+    logits = torch.randn((70, e + 1), generator=g, device=DEV).to(dt)
+    bias = 0.1 * torch.randn(e, generator=g, device=DEV)
+    for b in (bias, None):
+        for sigmoid in (True, False):
+            check_route(logits, k, oracle_mod, b, 1, sigmoid, groups, topk_groups)
+
+
+def test_route_ties_go_to_the_lower_index(oracle_mod):
+    """Equal logits (bf16 steps make many), equal groups, and biases that make unequal logits nearly equal."""
+    flat = torch.zeros((3, 130), device=DEV)
+    ids, w = check_route(flat, 5, oracle_mod)
+    assert (ids == np.arange(5)).all() and np.allclose(w, 0.2)
+    check_route(flat, 5, oracle_mod, torch.zeros(130, device=DEV), groups=13, topk_groups=2)
+    g = torch.Generator(device=DEV).manual_seed(5)
+    steps = torch.randint(-2, 3, (200, 256), generator=g, device=DEV).float()
+    for bias in (None, torch.zeros(256, device=DEV), torch.randint(0, 2, (256,), generator=g, device=DEV).float()):
+        for sigmoid in (True, False):
+            check_route(steps, 8, oracle_mod, bias, sigmoid=sigmoid)
+            check_route(steps, 8, oracle_mod, bias, sigmoid=sigmoid, groups=8, topk_groups=3)
+
+
+@pytest.mark.parametrize("sigmoid", [True, False])
+def test_route_values_fp32_cannot_tell_apart(sigmoid, oracle_mod):
+    """Biases that cancel the scores to within fp32's rounding, either way: the 64-bit order holds."""
+    r = np.random.default_rng(6)
+    n, e = 64, 64
+    logits = torch.from_numpy(r.standard_normal((1, e)).astype(np.float32)).repeat(n, 1)
+    l = logits[0].double().numpy()
+    s = 1 / (1 + np.exp(-l)) if sigmoid else np.exp(l) / np.exp(l).sum()
+    bias = torch.from_numpy((1.0 - s).astype(np.float32))  # score + bias = 1 but for the bias' rounding
+    # a row's logits moved by single steps, so that rows differ
+    moved = torch.nextafter(logits, torch.full_like(logits, 9.0))
+    logits = torch.where(torch.from_numpy(r.random((n, e)) < 0.5), moved, logits).to(DEV)
+    check_route(logits, 8, oracle_mod, bias.to(DEV), sigmoid=sigmoid)
+    check_route(logits, 8, oracle_mod, bias.to(DEV), sigmoid=sigmoid, groups=8, topk_groups=2)
+    check_route(logits, 8, oracle_mod, 5.0 + bias.to(DEV), sigmoid=sigmoid)
+
+
+@pytest.mark.parametrize("sigmoid", [True, False])
+def test_route_masks(sigmoid, oracle_mod):
+    """-inf, the types' lowest values, NaN and +inf; rows with fewer experts than slots, and with none."""
+    inf, nan, low = float("inf"), float("nan"), torch.finfo(F32).min
+    g = torch.Generator(device=DEV).manual_seed(7)
+    logits = torch.randn((8, 42), generator=g, device=DEV)
+    logits[0, 3:40] = -inf           # three experts left
+    logits[1, :] = -inf              # none, and no shared one
+    logits[2, :40] = nan             # only the shared ones
+    logits[3, 40] = -inf             # a masked shared expert
+    logits[4, 5:] = low              # masked by the lowest value: still chosen when nothing else is left
+    logits[5, ::2] = -inf
+    logits[6, :] = low
+    bias = 0.1 * torch.randn(40, generator=g, device=DEV)
+    for b in (None, bias):
+        for groups, kept in ((1, 1), (8, 3)):
+            for renorm in (True, False):
+                ids, w = check_route(logits, 6, oracle_mod, b, 2, sigmoid, groups, kept, renorm)
+                assert (ids[1] == -1).all() and (w[1] == 0).all()
+                assert np.isfinite(w).all()
+    ids, _ = run_route(logits, 6, None, 2, scoring=int(sigmoid))
+    assert ids[0].tolist()[3:6] == [-1, -1, -1] and ids[2].tolist() == [-1] * 6 + [40, 41]
+    hot = logits.clone()
+    hot[7, 9] = inf                  # counts as the largest finite value
+    ids, w = run_route(hot, 6, None, 2, scoring=int(sigmoid))
+    assert ids[7, 0] == 9 and np.isfinite(w[7]).all()
+    if not sigmoid:
+        assert w[7, 0] == 1.0 and (w[7, 1:] == 0).all()
+
+
+def test_route_small_scores_keep_their_ratios(oracle_mod):
+    """Sigmoids far below fp32's range: the renormalised weights are those of the formula."""
+    logits = torch.tensor([[-200.0, -201.0, -203.0, -260.0], [-90.0, -89.0, -95.0, -88.5]], device=DEV)
+    check_route(logits, 3, oracle_mod)
+    ids, w = run_route(logits, 2, None, 0)
+    assert abs(w[0, 0] - 1 / (1 + np.exp(-1.0))) < 1e-6
+
+
+def test_route_many_tokens_and_rows_behind(oracle_mod):
+    n = 148 * 64 * 4 * 2 + 3
+    g = torch.Generator(device=DEV).manual_seed(8)
+    logits = torch.randn((n, 9), generator=g, device=DEV)
+    ids = torch.full((n + 2, 3), -7, dtype=torch.int32, device=DEV)
+    w = torch.full((n + 2, 3), 9.0, device=DEV)
+    dmel.dmel_route(logits, ids[:n], w[:n], n_shared=1, renormalise=False)
+    top = torch.topk(logits[:, :8], 2, dim=1)
+    assert torch.equal(ids[:n, :2].long(), top.indices) and (ids[:n, 2] == 8).all()
+    ref = torch.sigmoid(torch.cat([top.values, logits[:, 8:]], 1).double())
+    assert ((w[:n].double() - ref).abs() <= 16 * 2.0 ** -24 * ref).all()
+    assert (ids[n:] == -7).all() and (w[n:] == 9.0).all()
+
+
+# ------------------------------------------------------------------------------ experts
+
+def expert_inputs(seed, n, slots, e, d, h, empty=0.0):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    x = torch.randn((n, d), generator=g, device=DEV).to(BF16)
+    w_in = (torch.randn((e, d, 2 * h), generator=g, device=DEV) / d ** 0.5).to(BF16)
+    w_out = (torch.randn((e, h, d), generator=g, device=DEV) / h ** 0.5).to(BF16)
+    ids = torch.randint(0, e, (n, slots), generator=g, device=DEV, dtype=torch.int32)
+    if empty:
+        ids[torch.rand((n, slots), generator=g, device=DEV) < empty] = -1
+    w = torch.randn((n, slots), generator=g, device=DEV)
+    return x, ids, w, w_in, w_out
+
+
+def run_experts(x, ids, w, w_in, w_out, stream=None, workspace=None):
+    e, h, d = w_out.shape
+    n, slots = ids.shape
+    if workspace is None:
+        # the scratch's old contents do not matter
+        workspace = torch.full((dmel.dmel_experts_workspace_size(n, slots, e, d, h),), 0xFF, dtype=torch.uint8, device=DEV)
+    out = torch.full((n, d), 5.0, dtype=BF16, device=DEV)
+    dmel.dmel_experts(x, ids, w, w_in, w_out, out, workspace, stream=stream)
+    return out
+
+
+def check_experts(x, ids, w, w_in, w_out, oracle_mod):
+    out = run_experts(x, ids, w, w_in, w_out)
+    assert dmel.dmel_last_launch_count() >= 1
+    masked = torch.where(ids >= 0, w, torch.zeros_like(w))
+    ref, _, spread = oracle_mod.experts(f64(x), ids.cpu().numpy(), f64(masked), f64(w_in), f64(w_out))
+    got = f64(out)
+    assert np.isfinite(got).all()
+    # no element beyond what the roundings can do together, and the whole as far off as independent
+    # roundings are: each uniform within half a step, 2^-8 / sqrt 3 of the value at most, for the gated
+    # row and the output
+    sums = ids.shape[1] * 2.0 ** -23 * np.abs(ref)
+    assert (np.abs(got - ref) <= 2.0 ** -8 * 1.01 * np.abs(ref) + 1.01 * spread + sums + 1e-37).all()
+    if ref.size >= 2000:
+        assert np.linalg.norm(got - ref) <= 1.25 * 2 ** 0.5 * 2.0 ** -8 / 3 ** 0.5 * np.linalg.norm(ref)
+    assert dmel.dmel_get_device_error(clear=True) == 0
+    return out
+
+
+@pytest.mark.parametrize("n,slots,e,d,h", [
+    (1, 1, 1, 8, 8), (1, 6, 32, 512, 128), (2, 3, 4, 72, 40), (5, 2, 3, 200, 264), (40, 2, 2, 136, 72),
+    (300, 2, 3, 264, 136), (257, 1, 1, 64, 64), (700, 3, 7, 328, 200), (64, 8, 96, 128, 64), (33, 64, 5, 64, 24),
+    (1100, 4, 2, 64, 520), (3, 2, 1024, 24, 16)])
+def test_experts(n, slots, e, d, h, oracle_mod):
+    check_experts(*expert_inputs(n + d, n, slots, e, d, h), oracle_mod)
+
+
+def test_experts_model_width(oracle_mod):
+    """6144 columns, 1,024 hidden: one token's six experts, and a step of 20 tokens."""
+    x, ids, w, w_in, w_out = expert_inputs(50, 20, 6, 8, 6144, 1024)
+    a = check_experts(x, ids, w, w_in, w_out, oracle_mod)
+    b = check_experts(x[:1].clone(), ids[:1].clone(), w[:1].clone(), w_in, w_out, oracle_mod)
+    assert (a[0].float() - b[0].float()).norm() <= 2.0 ** -7 * b[0].float().norm()
+
+
+def test_experts_exact_on_integers():
+    """One-hot tokens, gates of 64 (silu(64) is 64 in fp32) and small integers elsewhere: every product and
+    sum is exact, so each output is the exact value rounded once."""
+    for n, slots, e, d, h in ((3, 2, 4, 80, 56), (500, 3, 5, 344, 216), (90, 2, 64, 136, 72)):
+        g = torch.Generator(device=DEV).manual_seed(n)
+        at = torch.randint(0, d, (n,), generator=g, device=DEV)
+        x = torch.nn.functional.one_hot(at, d).to(BF16)
+        w_in = torch.randint(-1, 2, (e, d, 2 * h), generator=g, device=DEV).to(BF16)
+        w_in[:, :, :h] = 64.0
+        w_out = torch.randint(-1, 2, (e, h, d), generator=g, device=DEV).to(BF16)
+        ids = torch.randint(0, e, (n, slots), generator=g, device=DEV, dtype=torch.int32)
+        w = 2.0 ** torch.randint(-1, 2, (n, slots), generator=g, device=DEV)
+        up = w_in[ids.long(), at[:, None], h:].double()              # [n, slots, h]
+        ref = torch.zeros((n, d), dtype=torch.float64, device=DEV)
+        for j in range(slots):
+            ref += w[:, j:j + 1].double() * torch.bmm(64 * up[:, j:j + 1], w_out[ids[:, j].long()].double())[:, 0]
+        assert torch.equal(run_experts(x, ids, w, w_in, w_out), ref.float().to(BF16))
+
+
+def test_experts_empty_slots_and_bad_ids(oracle_mod):
+    x, ids, w, w_in, w_out = expert_inputs(60, 90, 3, 6, 136, 72, empty=0.4)
+    ids[5] = -1                      # a token without an expert: zeros
+    w[ids < 0] = float("nan")        # weights of empty slots are not read
+    out = check_experts(x, ids, w, w_in, w_out, oracle_mod)
+    assert (out[5] == 0).all()
+    assert (run_experts(x, torch.full_like(ids, -1), w, w_in, w_out) == 0).all()
+    bad = torch.where(ids < 0, 6, ids)
+    bad[7, 0] = -2
+    ref = torch.where((bad == 6) | (bad == -2), -1, bad)
+    wz = torch.nan_to_num(w)
+    assert torch.equal(run_experts(x, bad, wz, w_in, w_out), run_experts(x, ref, wz, w_in, w_out))
+    assert dmel.dmel_get_device_error(clear=True) & dmel.DMEL_DEVERR_EXPERT
+
+
+def test_experts_one_expert_for_all_and_twice_in_a_token(oracle_mod):
+    x, ids, w, w_in, w_out = expert_inputs(61, 290, 2, 9, 72, 40)
+    ids[:] = 4
+    out = check_experts(x, ids, w, w_in, w_out, oracle_mod)
+    # two slots of one expert add their weights
+    both = run_experts(x, ids[:, :1].contiguous(), w.sum(1, keepdim=True), w_in, w_out)
+    assert ((out.float() - both.float()).abs() <= 2.0 ** -6 * both.float().abs() + 1e-3).all()
+
+
+def test_experts_nan_stays_with_its_token():
+    x, ids, w, w_in, w_out = expert_inputs(62, 200, 2, 3, 200, 72)
+    clean = run_experts(x, ids, w, w_in, w_out)
+    x[77, 3] = float("nan")
+    x[78, 5] = float("inf")
+    out = run_experts(x, ids, w, w_in, w_out)
+    assert out[77].isnan().all()
+    rest = torch.ones(200, dtype=torch.bool, device=DEV)
+    rest[77:79] = False
+    assert torch.equal(out[rest], clean[rest])
+
+
+def test_experts_same_bits_every_time_and_rows_behind():
+    x, ids, w, w_in, w_out = expert_inputs(63, 600, 4, 7, 264, 136)
+    first = run_experts(x, ids, w, w_in, w_out)
+    big = torch.full((603, 264), 7.0, dtype=BF16, device=DEV)
+    ws = torch.zeros(dmel.dmel_experts_workspace_size(600, 4, 7, 264, 136), dtype=torch.uint8, device=DEV)
+    for _ in range(3):
+        dmel.dmel_experts(x, ids, w, w_in, w_out, big[:600], ws)
+        assert torch.equal(big[:600], first) and (big[600:] == 7.0).all()
+
+
+# ------------------------------------------------------------------------------ together, streams, graphs
+
+def block_step(s, x, state, ws, stream=None):
+    """One pass through the block: ShortConv, residual + norm, router, experts, residual + norm in 8 bits."""
+    kw = dict(stream=stream)
+    dmel.dmel_shortconv(x, s["off"], s["conv"], s["y"], state=state, state_out=state, **kw)
+    dmel.dmel_add_rmsnorm(s["y"], s["g1"], s["n1"], residual=s["stream"], residual_out=s["stream"], **kw)
+    logits = torch.matmul(s["n1"], s["router"]).float()
+    dmel.dmel_route(logits, s["ids"], s["wts"], n_shared=2, bias=s["bias"], **kw)
+    dmel.dmel_experts(s["n1"], s["ids"], s["wts"], s["w_in"], s["w_out"], s["moe"], ws, **kw)
+    dmel.dmel_add_rmsnorm(s["moe"], s["g2"], s["n2"], residual=s["stream"], residual_out=s["stream"], scales=s["sc"],
+                          scale_block=128, **kw)
+    return logits
+
+
+def block_state(seed, n, d=264, h=72, e=16, k=3):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    rn = lambda *shape, scale=1.0: scale * torch.randn(shape, generator=g, device=DEV)  # noqa: E731
+    return dict(off=torch.arange(n + 1, dtype=torch.int64, device=DEV), conv=rn(d, 4, scale=0.3), y=torch.empty((n, d), dtype=BF16, device=DEV),
+                g1=(1 + rn(d, scale=0.1)).to(BF16), g2=(1 + rn(d, scale=0.1)).to(BF16), n1=torch.empty((n, d), dtype=BF16, device=DEV),
+                stream=rn(n, d).to(BF16), router=rn(d, e + 2, scale=d ** -0.5).to(BF16), bias=rn(e, scale=0.05),
+                ids=torch.empty((n, k + 2), dtype=torch.int32, device=DEV), wts=torch.empty((n, k + 2), device=DEV),
+                w_in=rn(e + 2, d, 2 * h, scale=d ** -0.5).to(BF16), w_out=rn(e + 2, h, d, scale=h ** -0.5).to(BF16),
+                moe=torch.empty((n, d), dtype=BF16, device=DEV), n2=torch.empty((n, d), dtype=E4M3, device=DEV),
+                sc=torch.empty((n, -(-d // 128)), device=DEV)), rn(n, d).to(BF16), rn(n, 3, d).to(BF16)
+
+
+def workspace_for(s):
+    e, h, d = s["w_out"].shape
+    n, slots = s["ids"].shape
+    return torch.empty(dmel.dmel_experts_workspace_size(n, slots, e, d, h), dtype=torch.uint8, device=DEV)
+
+
+@pytest.mark.parametrize("n", [1, 5, 150])
+def test_block_against_the_oracle(n, oracle_mod):
+    """The run of calls a decoder layer makes, each against the oracle on what it was given."""
+    s, x, state = block_state(70 + n, n)
+    before, stream0 = state.clone(), s["stream"].clone()
+    # keep what the first norm leaves in the stream
+    dmel.dmel_shortconv(x, s["off"], s["conv"], s["y"], state=state.clone())
+    mid = torch.empty_like(stream0)
+    dmel.dmel_add_rmsnorm(s["y"], s["g1"], s["n1"], residual=stream0, residual_out=mid)
+    logits = block_step(s, x, state, workspace_for(s))
+    ry, _ = oracle_mod.shortconv(f64(x), s["off"].cpu().numpy(), f64(s["conv"]), f64(before))
+    assert (np.abs(f64(s["y"]) - ry) <= 2.0 ** -7 * (np.abs(ry) + 0.1)).all()
+    r1, y1 = oracle_mod.add_rmsnorm(f64(s["y"]), f64(stream0), f64(s["g1"]), 1e-6)
+    assert (np.abs(f64(mid) - r1) <= 2.0 ** -8 * 1.01 * np.abs(r1)).all()
+    assert (np.abs(f64(s["n1"]) - y1) <= (2.0 ** -8 * 1.01 + norm_bound(264)) * np.abs(y1)).all()
+    ids, _ = oracle_mod.route(f64(logits), 2, 3, True, f64(s["bias"]))
+    np.testing.assert_array_equal(s["ids"].cpu().numpy(), ids)
+    assert (s["ids"][:, 3:] == torch.tensor([16, 17], device=DEV)).all()
+    ref, _, spread = oracle_mod.experts(f64(s["n1"]), ids, f64(s["wts"]), f64(s["w_in"]), f64(s["w_out"]))
+    assert (np.abs(f64(s["moe"]) - ref) <= 2.0 ** -8 * 1.01 * np.abs(ref) + 1.01 * spread + 1e-6 * np.abs(ref)).all()
+    r2, y2, sc2 = oracle_mod.add_rmsnorm(f64(s["moe"]), f64(mid), f64(s["g2"]), 1e-6, 128)
+    assert (np.abs(f64(s["stream"]) - r2) <= 2.0 ** -8 * 1.01 * np.abs(r2)).all()
+    each = np.repeat(sc2, 128, axis=1)[:, :264]
+    q = y2 / each
+    assert (np.abs(f64(s["n2"].float()) - q) <= (2.0 ** -4 + 1e-5) * np.abs(q) + 2.0 ** -10).all()
+    assert dmel.dmel_get_device_error(clear=True) == 0
+
+
+def test_block_in_graphs_and_on_other_streams():
+    """Captured and replayed with new inputs, two graphs with a workspace each replayed at the same time on
+    two streams, and calls on a stream that is not the current one: the same bits as eager calls."""
+    runs = []
+    for seed in (80, 81):
+        s, x, state = block_state(seed, 37)
+        ws = workspace_for(s)
+        x2 = torch.roll(x, 1, 0)
+        want = []
+        first = {k: v.clone() for k, v in dict(stream=s["stream"], state=state).items()}
+        for xi in (x, x2):
+            block_step(s, xi, state, ws)
+            want.append({k: s[k].clone() for k in ("y", "n1", "ids", "wts", "moe", "stream", "sc")} | {"n2": s["n2"].view(torch.uint8).clone()})
+        s["stream"].copy_(first["stream"]); state.copy_(first["state"])
+        buf = x.clone()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            block_step(s, buf, state, ws, stream=torch.cuda.current_stream())
+        s["stream"].copy_(first["stream"]); state.copy_(first["state"])
+        runs.append((s, state, buf, (x, x2), want, graph, first, ws))
+
+    def same(s, w):
+        got = {k: s[k] for k in w if k != "n2"} | {"n2": s["n2"].view(torch.uint8)}
+        return all(torch.equal(got[k], w[k]) for k in w)
+
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for i in range(2):
+        for (s, state, buf, xs, want, graph, first, ws), st in zip(runs, streams):
+            with torch.cuda.stream(st):
+                buf.copy_(xs[i])
+                graph.replay()
+        torch.cuda.synchronize()
+        for s, state, buf, xs, want, graph, first, ws in runs:
+            assert same(s, want[i]), i
+    # eager on the side streams, given by argument for the library's calls
+    for s, state, buf, xs, want, graph, first, ws in runs:
+        s["stream"].copy_(first["stream"]); state.copy_(first["state"])
+    torch.cuda.synchronize()
+    for i in range(2):
+        for (s, state, buf, xs, want, graph, first, ws), st in zip(runs, streams):
+            with torch.cuda.stream(st):  # (torch.matmul of the step goes by the current stream)
+                block_step(s, xs[i], state, ws, stream=st)
+        torch.cuda.synchronize()
+        for s, state, buf, xs, want, graph, first, ws in runs:
+            assert same(s, want[i]), i
+    del runs
