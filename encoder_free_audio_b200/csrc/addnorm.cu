@@ -80,6 +80,8 @@ __device__ __forceinline__ void store8(__nv_fp8_e4m3 *p, const float (&v)[8]) {
   *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
 }
 
+__device__ __forceinline__ float scale_of(float amax) { return fmaxf(amax, kMinAmax) * (1.0f / kE4m3Max); }
+
 struct Add {
   __device__ float operator()(float a, float b) const { return a + b; }
 };
@@ -103,34 +105,53 @@ __device__ __forceinline__ float block_reduce(float v, float *slots, int warps, 
   return v;
 }
 
-// V pieces of 8 values per thread: piece j of thread t holds columns 8 (j blockDim + t) and on.
-template <typename T, typename TO, int V>
-__global__ void __launch_bounds__(1024) add_rmsnorm_kernel(const T *x, const T *res, int64_t n_rows, int dim, const T *__restrict__ w, float eps,
-                                   T *res_out, TO *out, float *scales, int scale_block) {
+// The e4m3 output's scales: `shift` is log2 of the pieces per block (2, 3, 4), or -1 for one scale per
+// row; n_blocks scales per row.
+struct Scales {
+  float *p;
+  int shift, n_blocks;
+};
+
+// V pieces of 8 values per thread: piece j of thread x holds columns 8 (j blockDim.x + x) and on.
+// With kWarpRows a row takes one warp and a block has blockDim.y of them, without barriers; else it
+// takes the block (and its address is the same in every thread, which saves registers).
+// Two pieces and 32 registers: what bounds the rate is how many threads an SM holds (2,048) and
+// then, for e4m3, the instructions per value. 24,000 x 6144 bf16 with the stream in and out: 183 us,
+// 6.4 TB/s (64 registers 198 us, one piece 230 us); 12,800 rows into e4m3 by 128 columns: 99 us.
+// With no more rows than SMs one piece is the shorter way (8 rows: 2.4 us against 3.0), and for fp32
+// rows, which have twice the bytes per piece, it is the faster one (1,601 x 5992: 25 us against 29).
+template <typename T, typename TO, int V, bool kWarpRows>
+__global__ void __launch_bounds__(1024, 2) add_rmsnorm_kernel(const T *x, const T *res, int64_t n_rows, int dim,
+                                                              const T *__restrict__ w, float eps, T *res_out, TO *out,
+                                                              Scales sc) {
   __shared__ float red[2][2][32];
-  const int warps = blockDim.x >> 5, pieces = dim >> 3;
+  const int warps = kWarpRows ? 1 : blockDim.x >> 5, pieces = dim >> 3;
+  const float inv_dim = 1.0f / (float)dim;
+  const int64_t step = (int64_t)gridDim.x * (kWarpRows ? blockDim.y : 1);
   int turn = 0;  // two sets of slots: a row's second use of one is a barrier away from its first
-  for (int64_t row = blockIdx.x; row < n_rows; row += gridDim.x, turn ^= 1) {
-    const int64_t base = row * dim;
+  for (int64_t row = kWarpRows ? (int64_t)blockIdx.x * blockDim.y + threadIdx.y : blockIdx.x; row < n_rows;
+       row += step, turn ^= 1) {
+    const T *xr = x + row * dim;
     float s[V][8];
     float ss = 0.0f;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      const int p = j * blockDim.x + threadIdx.x;
-      if (p < pieces) {
-        load8(x + base + 8 * p, s[j]);
+      const uint32_t p = j * blockDim.x + threadIdx.x;
+      if (p < (uint32_t)pieces) {
+        load8(xr + 8u * p, s[j]);
       } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i) s[j][i] = 0.0f;
       }
     }
     if (res) {
+      const T *rr = res + row * dim;
 #pragma unroll
       for (int j = 0; j < V; ++j) {
-        const int p = j * blockDim.x + threadIdx.x;
-        if (p < pieces) {
+        const uint32_t p = j * blockDim.x + threadIdx.x;
+        if (p < (uint32_t)pieces) {
           float r[8];
-          load8(res + base + 8 * p, r);
+          load8(rr + 8u * p, r);
 #pragma unroll
           for (int i = 0; i < 8; ++i) s[j][i] += r[i];
         }
@@ -142,27 +163,34 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_kernel(const T *x, const T *
       for (int i = 0; i < 8; ++i) ss = fmaf(s[j][i], s[j][i], ss);
     }
     if (res_out) {
+      T *ro = res_out + row * dim;
 #pragma unroll
       for (int j = 0; j < V; ++j) {
-        const int p = j * blockDim.x + threadIdx.x;
-        if (p < pieces) store8(res_out + base + 8 * p, s[j]);
+        const uint32_t p = j * blockDim.x + threadIdx.x;
+        if (p < (uint32_t)pieces) store8(ro + 8u * p, s[j]);
       }
     }
     ss = block_reduce(ss, red[turn][0], warps, Add());
-    const float rstd = 1.0f / sqrtf(ss / (float)dim + eps);
+    const float rstd = rsqrtf(fmaf(ss, inv_dim, eps));  // (within 2 ulps, on the special-function unit)
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      const int p = j * blockDim.x + threadIdx.x;
-      if (p < pieces) {
+      const uint32_t p = j * blockDim.x + threadIdx.x;
+      if (p < (uint32_t)pieces) {
         float g[8];
-        weight8(w + 8 * p, g);
+        weight8(w + 8u * p, g);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s[j][i] = s[j][i] * rstd * g[i];
+        for (int i = 0; i < 8; ++i) s[j][i] *= g[i];
       }
     }
+    float mult[V];  // what w s is multiplied by
+#pragma unroll
+    for (int j = 0; j < V; ++j) mult[j] = rstd;
     if (sizeof(TO) == 1) {
       // largest magnitude of each piece, then of its block: 4, 8 or 16 neighbouring threads (the
-      // block's pieces, since blockDim is a multiple of 32), or the whole row. fmaxf drops NaN.
+      // block's pieces, since blockDim.x is a multiple of 32), or the whole row. fmaxf drops NaN.
+      // w s / sqrt(..) / scale is a product with an approximate reciprocal of the scale, which is far
+      // from the ends of fp32's range: a few ulps before a rounding to 4 bits, and the block's
+      // largest value, within those of 448, becomes 448.
       float top[V];
 #pragma unroll
       for (int j = 0; j < V; ++j) {
@@ -170,53 +198,62 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_kernel(const T *x, const T *
 #pragma unroll
         for (int i = 0; i < 8; ++i) top[j] = fmaxf(top[j], fabsf(s[j][i]));
       }
-      if (scale_block == 0) {
+      if (sc.shift < 0) {
         float m = top[0];
 #pragma unroll
         for (int j = 1; j < V; ++j) m = fmaxf(m, top[j]);
-        m = block_reduce(m, red[turn][1], warps, Max());
+        const float scale = scale_of(rstd * block_reduce(m, red[turn][1], warps, Max()));
 #pragma unroll
-        for (int j = 0; j < V; ++j) top[j] = m;
-        if (threadIdx.x == 0) scales[row] = fmaxf(m, kMinAmax) / kE4m3Max;
+        for (int j = 0; j < V; ++j) mult[j] = rstd * __fdividef(1.0f, scale);
+        if (threadIdx.x == 0) sc.p[row] = scale;
       } else {
-        const int per = scale_block >> 3, n_blocks = (pieces + per - 1) / per;
+        float *row_scales = sc.p + row * sc.n_blocks;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-          for (int o = 1; o < per; o <<= 1) top[j] = fmaxf(top[j], __shfl_xor_sync(0xffffffffu, top[j], o));
-          const int p = j * blockDim.x + threadIdx.x;
-          if (p < pieces && p % per == 0) scales[row * n_blocks + p / per] = fmaxf(top[j], kMinAmax) / kE4m3Max;
+          top[j] = fmaxf(top[j], __shfl_xor_sync(0xffffffffu, top[j], 1));
+          top[j] = fmaxf(top[j], __shfl_xor_sync(0xffffffffu, top[j], 2));
+          if (sc.shift > 2) top[j] = fmaxf(top[j], __shfl_xor_sync(0xffffffffu, top[j], 4));
+          if (sc.shift > 3) top[j] = fmaxf(top[j], __shfl_xor_sync(0xffffffffu, top[j], 8));
+          const uint32_t p = j * blockDim.x + threadIdx.x;
+          const float scale = scale_of(rstd * top[j]);
+          mult[j] = rstd * __fdividef(1.0f, scale);
+          if (p < (uint32_t)pieces && (p & ((1u << sc.shift) - 1u)) == 0) row_scales[p >> sc.shift] = scale;
         }
       }
-#pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const float scale = fmaxf(top[j], kMinAmax) / kE4m3Max;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) s[j][i] = s[j][i] / scale;
-      }
     }
+    TO *orow = out + row * dim;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      const int p = j * blockDim.x + threadIdx.x;
-      if (p < pieces) store8(out + base + 8 * p, s[j]);
+      const uint32_t p = j * blockDim.x + threadIdx.x;
+      if (p < (uint32_t)pieces) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s[j][i] *= mult[j];
+        store8(orow + 8u * p, s[j]);
+      }
     }
   }
 }
 
 template <typename T, typename TO>
 cudaError_t launch_typed(const void *x, const void *res, int64_t n_rows, int dim, const void *w, float eps,
-                         void *res_out, void *out, float *scales, int scale_block, int num_sms, cudaStream_t stream) {
-  // up to 1024 threads with one piece each, or two pieces for rows above 8192 values
-  const int pieces = dim / 8, v = pieces > 1024 ? 2 : 1;
-  const int threads = ((pieces + v - 1) / v + 31) / 32 * 32;
-  const int64_t cap = (int64_t)num_sms * 64;
-  const unsigned grid = (unsigned)(n_rows < cap ? n_rows : cap);
+                         void *res_out, void *out, Scales sc, int num_sms, cudaStream_t stream) {
+  const int pieces = dim / 8;
+  const bool two = pieces > 1024 || (sizeof(T) == 2 && n_rows > num_sms);
+  const int threads = ((two ? (pieces + 1) / 2 : pieces) + 31) / 32 * 32;
+  const bool warp_rows = threads == 32;
+  const dim3 block(threads, warp_rows ? 8 : 1);
+  const int64_t blocks = (n_rows + block.y - 1) / block.y, cap = (int64_t)num_sms * 64;
+  const unsigned grid = (unsigned)(blocks < cap ? blocks : cap);
   const T *xt = static_cast<const T *>(x), *rt = static_cast<const T *>(res), *wt = static_cast<const T *>(w);
   T *so = static_cast<T *>(res_out);
   TO *ot = static_cast<TO *>(out);
-  if (v == 1)
-    add_rmsnorm_kernel<T, TO, 1><<<grid, threads, 0, stream>>>(xt, rt, n_rows, dim, wt, eps, so, ot, scales, scale_block);
-  else
-    add_rmsnorm_kernel<T, TO, 2><<<grid, threads, 0, stream>>>(xt, rt, n_rows, dim, wt, eps, so, ot, scales, scale_block);
+#define DMEL_NORM(V, ROWS) \
+  add_rmsnorm_kernel<T, TO, V, ROWS><<<grid, block, 0, stream>>>(xt, rt, n_rows, dim, wt, eps, so, ot, sc)
+  if (warp_rows && two) DMEL_NORM(2, true);
+  else if (warp_rows) DMEL_NORM(1, true);
+  else if (two) DMEL_NORM(2, false);
+  else DMEL_NORM(1, false);
+#undef DMEL_NORM
   return cudaGetLastError();
 }
 
@@ -225,8 +262,11 @@ cudaError_t launch_typed(const void *x, const void *res, int64_t n_rows, int dim
 cudaError_t launch_add_rmsnorm(const void *x, const void *residual, int64_t n_rows, int dim, dmel_dtype dtype,
                                const void *w, float eps, void *residual_out, void *out, dmel_dtype out_dtype,
                                float *scales, int scale_block, int num_sms, cudaStream_t stream, int *launches) {
-#define DMEL_NORM(T, TO) \
-  launch_typed<T, TO>(x, residual, n_rows, dim, w, eps, residual_out, out, scales, scale_block, num_sms, stream)
+  Scales sc;
+  sc.p = scales;
+  sc.shift = scale_block == 0 ? -1 : scale_block == 32 ? 2 : scale_block == 64 ? 3 : 4;
+  sc.n_blocks = scale_block == 0 ? 1 : (dim + scale_block - 1) / scale_block;
+#define DMEL_NORM(T, TO) launch_typed<T, TO>(x, residual, n_rows, dim, w, eps, residual_out, out, sc, num_sms, stream)
   cudaError_t e;
   if (dtype == DMEL_BF16)
     e = out_dtype == DMEL_E4M3   ? DMEL_NORM(__nv_bfloat16, __nv_fp8_e4m3)
