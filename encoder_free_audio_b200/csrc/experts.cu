@@ -35,10 +35,13 @@ struct TokenTile {
 
 // ---------------------------------------------------------------- plan
 //
-// The slots in expert order, stable, by counting: warp w counts its chunk of slots per expert, a
-// scan over (expert, warp) turns the counts into row numbers, and the same walk hands them out.
-// One block: at 24,576 slots it takes a few microseconds against about a millisecond of products.
+// The slots in expert order, stable, by counting: a warp counts its chunk of slots per expert, a
+// scan over (expert, block, warp) turns the counts into row numbers, and the same walk hands them
+// out. Bound by the matching of 32 slots at a time (about 190 cycles of a scheduler each): one
+// block for few slots, else a cluster of eight that read each other's counts (24,576 slots:
+// 38 us with one block).
 constexpr int kPlanThreads = 1024;
+constexpr int kAhead = 8;  // slots per lane whose ids are loaded before any is counted
 
 struct PlanOut {
   int *n_tiles;      // [1]
@@ -50,29 +53,38 @@ struct PlanOut {
 __global__ void __launch_bounds__(kPlanThreads) experts_plan_kernel(const int32_t *__restrict__ ids, int n_slots,
                                                                     int slots, int E, int tile_tokens, PlanOut out,
                                                                     uint32_t *err) {
-  extern __shared__ int hist[];  // [32 warps][E], then the experts' first rows [E]
+  extern __shared__ int hist[];  // [32 warps][E], the block's totals [E], the experts' first rows [E]
   __shared__ unsigned long long warp_sum[32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int *first = hist + 32 * E;
+  int *total = hist + 32 * E, *first = total + E;
+  const unsigned block = cluster_ctarank(), blocks = gridDim.x;  // one cluster
+  launch_dependents();
   for (int i = threadIdx.x; i < 32 * E; i += kPlanThreads) hist[i] = 0;
   __syncthreads();
-  const int chunk = ((n_slots + 31) / 32 + 31) / 32 * 32;  // slots per warp (n_slots <= 2^30)
-  const int begin = warp * chunk < n_slots ? warp * chunk : n_slots;
+  // slots per warp, a multiple of 32 (n_slots <= 2^30)
+  const int walkers = 32 * (int)blocks, chunk = ((n_slots + walkers - 1) / walkers + 31) / 32 * 32;
+  const int walker = (int)block * 32 + warp;
+  const int begin = (int64_t)walker * chunk < n_slots ? walker * chunk : n_slots;
   const int end = n_slots - begin < chunk ? n_slots : begin + chunk;
   auto expert_at = [&](int i) {
     if (i >= end) return -1;
     const int e = ids[i];
     return e >= 0 && e < E ? e : -1;
   };
-  for (int i = begin; i < end; i += 32) {
-    const int e = expert_at(i + lane);
-    const unsigned peers = __match_any_sync(kAll, e);
-    if (e >= 0 && lane == __ffs(peers) - 1) hist[warp * E + e] += __popc(peers);
-    __syncwarp();
+  for (int i = begin; i < end; i += 32 * kAhead) {
+    int e[kAhead];
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a) e[a] = expert_at(i + 32 * a + lane);
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a) {
+      const unsigned peers = __match_any_sync(kAll, e[a]);
+      if (e[a] >= 0 && lane == __ffs(peers) - 1) hist[warp * E + e[a]] += __popc(peers);
+      __syncwarp();
+    }
   }
   __syncthreads();
-  // counts -> exclusive row offsets within the expert, per warp; and the expert's total
-  int count = 0, tiles = 0;
+  // counts -> exclusive row offsets within the expert, per warp of this block; then over the blocks
+  int count = 0, tiles = 0, before_block = 0;
   const int e_mine = threadIdx.x;  // E <= 1024
   if (e_mine < E) {
     for (int w = 0; w < 32; ++w) {
@@ -80,8 +92,22 @@ __global__ void __launch_bounds__(kPlanThreads) experts_plan_kernel(const int32_
       hist[w * E + e_mine] = count;
       count += c;
     }
-    tiles = (count + tile_tokens - 1) / tile_tokens;
+    total[e_mine] = count;
   }
+  __syncwarp();
+  if (blocks > 1) {
+    cluster_sync();
+    if (e_mine < E) {
+      count = 0;
+      for (unsigned q = 0; q < blocks; ++q) {
+        if (q == block) before_block = count;
+        count += (int)ld_cluster_u32(mapa_shared(smem_addr(total + e_mine), q));
+      }
+    }
+    __syncwarp();
+    cluster_sync();  // (no block leaves, or reuses its totals, while another reads them)
+  }
+  tiles = (count + tile_tokens - 1) / tile_tokens;
   // exclusive scan of {tiles, rows} over the experts
   const unsigned long long own = ((unsigned long long)tiles << 32) | (unsigned)count;
   unsigned long long run = own;
@@ -105,8 +131,8 @@ __global__ void __launch_bounds__(kPlanThreads) experts_plan_kernel(const int32_
   const unsigned long long before = run - own + (warp > 0 ? warp_sum[warp - 1] : 0ull);
   if (e_mine < E) {
     const int row0 = (int)(unsigned)before, tile0 = (int)(before >> 32);
-    first[e_mine] = row0;
-    if (tiles > 0) {
+    first[e_mine] = row0 + before_block;
+    if (tiles > 0 && block == 0) {
       const int width = ((count + tiles - 1) / tiles + 15) / 16 * 16;
       for (int m = 0; m < tiles; ++m) {
         const int left = count - m * width, rows = left < width ? left : width;
@@ -119,20 +145,26 @@ __global__ void __launch_bounds__(kPlanThreads) experts_plan_kernel(const int32_
       }
     }
   }
-  if (threadIdx.x == kPlanThreads - 1) *out.n_tiles = (int)((before + own) >> 32);
+  if (threadIdx.x == kPlanThreads - 1 && block == 0) *out.n_tiles = (int)((before + own) >> 32);
   __syncthreads();
-  for (int i = begin; i < end; i += 32) {
-    const int e = expert_at(i + lane);
-    const unsigned peers = __match_any_sync(kAll, e);
-    int pos = -1;
-    if (e >= 0) pos = first[e] + hist[warp * E + e] + __popc(peers & ((1u << lane) - 1u));
-    __syncwarp();
-    if (e >= 0 && lane == __ffs(peers) - 1) hist[warp * E + e] += __popc(peers);
-    __syncwarp();
-    if (i + lane < end) {
-      out.row[i + lane] = pos;
-      if (pos >= 0) out.token[pos] = (i + lane) / slots;
-      else if (ids[i + lane] != -1) record_error(err, DMEL_DEVERR_EXPERT);
+  for (int i = begin; i < end; i += 32 * kAhead) {
+    int e[kAhead];
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a) e[a] = expert_at(i + 32 * a + lane);
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a) {
+      const unsigned peers = __match_any_sync(kAll, e[a]);
+      int pos = -1;
+      if (e[a] >= 0) pos = first[e[a]] + hist[warp * E + e[a]] + __popc(peers & ((1u << lane) - 1u));
+      __syncwarp();
+      if (e[a] >= 0 && lane == __ffs(peers) - 1) hist[warp * E + e[a]] += __popc(peers);
+      __syncwarp();
+      const int slot = i + 32 * a + lane;
+      if (slot < end) {
+        out.row[slot] = pos;
+        if (pos >= 0) out.token[pos] = slot / slots;
+        else if (ids[slot] != -1) record_error(err, DMEL_DEVERR_EXPERT);
+      }
     }
   }
 }
@@ -150,15 +182,22 @@ struct EX {
   static constexpr int B_STAGE = kTokens / 2 * BK * 2; // this CTA's half of the tokens
   static constexpr int STG_TOKENS = 32;
   static constexpr int STG = STG_TOKENS * 128 * 4;     // 32 tokens x 128 columns, fp32
-  static constexpr int BUDGET = 227 * 1024 - 1024 - 512 - 2 * STG;
+  static constexpr int IDX = kTokens / 2 * 4;          // row numbers of the half, for the gather warps
+  static constexpr int BUDGET = 227 * 1024 - 1024 - 512 - IDX - 2 * STG;
   static constexpr int STAGES = BUDGET / (A_STAGE + B_STAGE);
   static constexpr int OFF_B = STAGES * A_STAGE;
   static constexpr int OFF_STG = OFF_B + STAGES * B_STAGE;
   static constexpr int OFF_BAR = OFF_STG + 2 * STG;
   static constexpr int N_BARS = 2 * STAGES + 4 + 1;
-  static constexpr int SMEM_BYTES = OFF_BAR + 512 + 1024;
+  static constexpr int OFF_IDX = OFF_BAR + 512;
+  static constexpr int SMEM_BYTES = OFF_IDX + IDX + 1024;
   static constexpr int EPI_WARPS = 4;
-  static constexpr int THREADS = 32 * (2 + EPI_WARPS);  // warp 0 TMA, warp 1 MMA, warps 2..5 epilogue
+  // warp 0 TMA, warp 1 MMA, warps 2..5 epilogue, and for the gate and up products gather warps:
+  // one for narrow tiles, four for wide ones (4,096 tokens of 6 slots, 6144 x 2 x 1024: 971 us
+  // with two, 624 with four, 602 with plain boxes of rows in their place)
+  static constexpr int GATHER_WARPS = kTokens > 64 ? 4 : 1;
+  static constexpr int THREADS = 32 * (2 + EPI_WARPS);
+  static constexpr int THREADS_GATE = THREADS + 32 * GATHER_WARPS;
   static constexpr uint32_t ACC_STRIDE = kTokens;
   static constexpr uint32_t TMEM_COLS = 2 * kTokens < 32 ? 32 : 2 * kTokens;
   static_assert(kTokens % 32 == 0 && kTokens <= 256 && (TMEM_COLS & (TMEM_COLS - 1)) == 0, "token tile");
@@ -173,10 +212,11 @@ __device__ __forceinline__ float4 silu_times(float4 g, float4 u) {
 }
 
 template <int kTokens, bool kGate>
-__global__ void __launch_bounds__(EX<kTokens>::THREADS, 1)
+__global__ void __launch_bounds__(kGate ? EX<kTokens>::THREADS_GATE : EX<kTokens>::THREADS, 1)
     experts_product_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
-                           const int *__restrict__ n_tiles, const TokenTile *__restrict__ tiles,
-                           const int *__restrict__ token, int K, int cols, void *__restrict__ out, uint32_t *err) {
+                           const __grid_constant__ CUtensorMap xmap8, const int *__restrict__ n_tiles,
+                           const TokenTile *__restrict__ tiles, const int *__restrict__ token, int K, int cols,
+                           void *__restrict__ out, uint32_t *err) {
   using X = EX<kTokens>;
   constexpr int STAGES = X::STAGES, BK = X::BK;
   constexpr int COLS = kGate ? 64 : 128;  // columns of the output per CTA
@@ -217,6 +257,9 @@ __global__ void __launch_bounds__(EX<kTokens>::THREADS, 1)
   cluster_sync();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_holder;
+  // (Letting the down product load its first weights before this wait measured the same.)
+  wait_for_predecessors();
+  launch_dependents();
 
   const int n_ct = (cols + 2 * COLS - 1) / (2 * COLS);  // column tiles
   const int64_t total = (int64_t)*n_tiles * n_ct;
@@ -226,7 +269,7 @@ __global__ void __launch_bounds__(EX<kTokens>::THREADS, 1)
   auto tile_at = [&](int64_t t) { return tiles[t / n_ct]; };
 
   if (warp == 0) {
-    // ------------------------------------------------ TMA: this CTA's weight boxes and token rows
+    // ------------------------------------------------ TMA: weight boxes, and consecutive rows
     int stage = 0;
     uint32_t phase = 0, pending = 0, pending_phase = 0;
     bool ok = true;
@@ -234,26 +277,26 @@ __global__ void __launch_bounds__(EX<kTokens>::THREADS, 1)
       const TokenTile tt = tile_at(t);
       const int col = (int)(t % n_ct) * 2 * COLS + (int)rank * COLS;
       const int half = tt.width / 2;  // token rows of this CTA, a multiple of 8
-      // lane g gathers rows 4 g .. 4 g + 3 of the half; rows past the tile repeat its last one
-      int r[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        int q = (int)rank * half + 4 * lane + i;
-        q = tt.row0 + (q < tt.rows ? q : tt.rows - 1);
-        r[i] = kGate ? token[q] : q;
-      }
       const uint32_t bytes = 2u * (X::A_STAGE + (uint32_t)half * 128u);
       for (int kb = 0; kb < KB; ++kb) {
         if (!__all_sync(kAll, mbar_wait(empty(stage), phase ^ 1u, err))) { ok = false; break; }
-        if (leader && lane == 0) mbar_arrive_expect_tx(full(stage), bytes);
+        if (elect_one()) {
+          if (leader) mbar_arrive_expect_tx(full(stage), bytes);
+          const uint32_t fb = mapa_shared(full(stage), 0);
+          const uint32_t a_dst = smem_addr(smem + stage * X::A_STAGE);
+          // kGate: the gate's box, then the up box `cols` further on
+          tma_load_3d_pair(a_dst, &wmap, col, kb * BK, tt.expert, fb);
+          tma_load_3d_pair(a_dst + X::BOX, &wmap, col + (kGate ? cols : 64), kb * BK, tt.expert, fb);
+          if (!kGate) {
+            // rows past the tile are the next expert's, or zeros past the last: computed, not stored
+            const uint32_t b_dst = smem_addr(smem + X::OFF_B + stage * X::B_STAGE);
+            const int row = tt.row0 + (int)rank * half;
+            int r = 0;
+            for (; r + 32 <= half; r += 32) tma_load_2d_pair(b_dst + r * 128, &xmap, kb * BK, row + r, fb);
+            for (; r < half; r += 8) tma_load_2d_pair(b_dst + r * 128, &xmap8, kb * BK, row + r, fb);
+          }
+        }
         __syncwarp();
-        const uint32_t fb = mapa_shared(full(stage), 0);
-        const uint32_t a_dst = smem_addr(smem + stage * X::A_STAGE);
-        if (lane < 2)  // kGate: the gate's box, then the up box `cols` further on
-          tma_load_3d_pair(a_dst + lane * X::BOX, &wmap, col + lane * (kGate ? cols : 64), kb * BK, tt.expert, fb);
-        if (4 * lane < half)
-          tma_gather4_pair(smem_addr(smem + X::OFF_B + stage * X::B_STAGE) + lane * 512, &xmap, kb * BK, r[0], r[1], r[2],
-                           r[3], fb);
         pending |= 1u << stage;
         pending_phase = (pending_phase & ~(1u << stage)) | (phase << stage);
         if (++stage == STAGES) { stage = 0; phase ^= 1u; }
@@ -265,37 +308,79 @@ __global__ void __launch_bounds__(EX<kTokens>::THREADS, 1)
         if (pending & (1u << s)) mbar_wait(full(s), (pending_phase >> s) & 1u, err);
   } else if (warp == 1) {
     // ------------------------------------------------ MMA issuer (even CTA)
-    if (leader && lane == 0) {
+    if (leader) {
       int stage = 0;
       uint32_t phase = 0, i = 0;
       bool ok = true;
       for (int64_t t = blockIdx.x >> 1; ok && t < total; t += step, ++i) {
         const uint32_t acc = i & 1u, use = i >> 1;
         const uint32_t idesc = idesc_bf16_f32(256, (uint32_t)tile_at(t).width, 0, 1);
-        if (!mbar_wait(tempty(acc), (use & 1u) ^ 1u, err)) break;
+        if (!__all_sync(kAll, mbar_wait(tempty(acc), (use & 1u) ^ 1u, err))) break;
         tc_fence_after();
         const uint32_t d = tmem_base + acc * X::ACC_STRIDE;
         for (int kb = 0; kb < KB; ++kb) {
-          if (!mbar_wait(full(stage), phase, err)) { ok = false; break; }
+          if (!__all_sync(kAll, mbar_wait(full(stage), phase, err))) { ok = false; break; }
           tc_fence_after();
           const uint32_t a0 = smem_addr(smem + stage * X::A_STAGE);
           const uint32_t b0 = smem_addr(smem + X::OFF_B + stage * X::B_STAGE);
+          if (elect_one()) {
 #pragma unroll
-          for (int k = 0; k < BK / 16; ++k) {
-            // weights: MN-major, 64-column boxes BOX apart, 8 K-rows 1024 B apart, 16 (2 KB) per step
-            const uint64_t adesc = smem_desc(a0 + 2048u * k, (uint32_t)X::BOX, 1024u, kSwizzle128B);
-            // tokens: K-major, 8-row groups 1024 B apart, 32 B per step
-            const uint64_t bdesc = smem_desc(b0 + 32u * k, 16u, 1024u, kSwizzle128B);
-            tc_mma_f16_pair(d, adesc, bdesc, idesc, (kb | k) != 0 ? 1u : 0u);
+            for (int k = 0; k < BK / 16; ++k) {
+              // weights: MN-major, 64-column boxes BOX apart, 8 K-rows 1024 B apart, 16 (2 KB) per step
+              const uint64_t adesc = smem_desc(a0 + 2048u * k, (uint32_t)X::BOX, 1024u, kSwizzle128B);
+              // tokens: K-major, 8-row groups 1024 B apart, 32 B per step
+              const uint64_t bdesc = smem_desc(b0 + 32u * k, 16u, 1024u, kSwizzle128B);
+              tc_mma_f16_pair(d, adesc, bdesc, idesc, (kb | k) != 0 ? 1u : 0u);
+            }
+            tc_commit_pair_both(empty(stage), 3);
           }
-          tc_commit_pair_both(empty(stage), 3);
+          __syncwarp();
           if (++stage == STAGES) { stage = 0; phase ^= 1u; }
         }
         if (!ok) break;
-        tc_commit_pair_both(tfull(acc), 3);
+        if (elect_one()) tc_commit_pair_both(tfull(acc), 3);
+        __syncwarp();
       }
-      tc_commit_pair(done_bar);
+      if (elect_one()) tc_commit_pair(done_bar);
+      __syncwarp();
       mbar_wait(done_bar, 0, err);
+    }
+  } else if (kGate && warp >= 2 + X::EPI_WARPS) {
+    // ------------------------------------------------ gather: token rows four at a time, by number
+    // Gather warp w takes every other group of four rows of this CTA's half.
+    const int w = warp - 2 - X::EPI_WARPS;
+    int4 *idx = reinterpret_cast<int4 *>(smem + X::OFF_IDX);
+    int stage = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int64_t t = blockIdx.x >> 1; ok && t < total; t += step) {
+      const TokenTile tt = tile_at(t);
+      const int groups = tt.width / 8;  // of four rows, in this CTA's half
+      __syncwarp();                     // the last tile's numbers have been read
+      for (int g = w + X::GATHER_WARPS * lane; g < groups; g += X::GATHER_WARPS * 32) {
+        int r[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int q = (int)rank * (tt.width / 2) + 4 * g + i;  // past the tile: its last row again
+          r[i] = token[tt.row0 + (q < tt.rows ? q : tt.rows - 1)];
+        }
+        idx[g] = make_int4(r[0], r[1], r[2], r[3]);
+      }
+      __syncwarp();
+      for (int kb = 0; kb < KB; ++kb) {
+        if (!__all_sync(kAll, mbar_wait(empty(stage), phase ^ 1u, err))) { ok = false; break; }
+        if (elect_one()) {
+          const uint32_t fb = mapa_shared(full(stage), 0);
+          const uint32_t b_dst = smem_addr(smem + X::OFF_B + stage * X::B_STAGE);
+#pragma unroll 4
+          for (int g = w; g < groups; g += X::GATHER_WARPS) {
+            const int4 r = idx[g];
+            tma_gather4_pair(b_dst + g * 512, &xmap, kb * BK, r.x, r.y, r.z, r.w, fb);
+          }
+        }
+        __syncwarp();
+        if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+      }
     }
   } else {
     // ------------------------------------------------ epilogue: lane = one M row (weight column)
@@ -370,6 +455,7 @@ __global__ void __launch_bounds__(EX<kTokens>::THREADS, 1)
 __global__ void __launch_bounds__(256) experts_sum_kernel(const float *__restrict__ y, const int *__restrict__ row,
                                                           const float *__restrict__ weights, int64_t n_tokens, int slots,
                                                           int dim, __nv_bfloat16 *__restrict__ out) {
+  wait_for_predecessors();
   const int pieces = dim / 8;
   const int64_t total = n_tokens * pieces;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
@@ -433,11 +519,11 @@ bool weight_map(CUtensorMap *map, EncodeTiledFn enc, const void *base, int E, in
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Rows [R][K] (K contiguous) for gathering: a box is 64 values of one row.
-bool row_map(CUtensorMap *map, EncodeTiledFn enc, const void *base, int64_t R, int K) {
+// Rows [R][K] (K contiguous) in boxes of 64 values of box_rows rows (1 for gathering).
+bool row_map(CUtensorMap *map, EncodeTiledFn enc, const void *base, int64_t R, int K, unsigned box_rows) {
   const cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)R};
   const cuuint64_t strides[1] = {(cuuint64_t)K * 2};
-  const cuuint32_t box[2] = {64, 1};
+  const cuuint32_t box[2] = {64, box_rows};
   const cuuint32_t estr[2] = {1, 1};
   return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base), dims, strides, box, estr,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -445,8 +531,8 @@ bool row_map(CUtensorMap *map, EncodeTiledFn enc, const void *base, int64_t R, i
 }
 
 template <int kTokens, bool kGate>
-cudaError_t launch_product(const CUtensorMap &wmap, const CUtensorMap &xmap, const int *n_tiles,
-                           const TokenTile *tiles, const int *token, int K, int cols, void *out, int64_t max_tiles,
+cudaError_t launch_product(const CUtensorMap &wmap, const CUtensorMap &xmap, const CUtensorMap &xmap8,
+                           const int *n_tiles, const TokenTile *tiles, const int *token, int K, int cols, void *out, int64_t max_tiles,
                            uint32_t *err, int num_sms, cudaStream_t stream) {
   using X = EX<kTokens>;
   static std::atomic<bool> attr[256];
@@ -456,17 +542,19 @@ cudaError_t launch_product(const CUtensorMap &wmap, const CUtensorMap &xmap, con
   const int64_t work = max_tiles * ((cols + per_pair - 1) / per_pair), pairs = num_sms / 2 > 0 ? num_sms / 2 : 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(2 * (work < pairs ? work : pairs)));
-  cfg.blockDim = dim3(X::THREADS);
+  cfg.blockDim = dim3(kGate ? X::THREADS_GATE : X::THREADS);
   cfg.dynamicSmemBytes = X::SMEM_BYTES;
   cfg.stream = stream;
-  cudaLaunchAttribute at[1];
+  cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeClusterDimension;
   at[0].val.clusterDim.x = 2;
   at[0].val.clusterDim.y = 1;
   at[0].val.clusterDim.z = 1;
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, experts_product_kernel<kTokens, kGate>, wmap, xmap, n_tiles, tiles, token, K, cols,
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, experts_product_kernel<kTokens, kGate>, wmap, xmap, xmap8, n_tiles, tiles, token, K, cols,
                             out, err);
 }
 
@@ -489,27 +577,42 @@ cudaError_t launch_experts(const void *x, int64_t n_tokens, const int32_t *ids, 
   plan.tiles = reinterpret_cast<TokenTile *>(base + L.tiles);
   plan.token = reinterpret_cast<int *>(base + L.token);
   plan.row = reinterpret_cast<int *>(base + L.row);
-  CUtensorMap in_w, in_x, out_w, out_h;
+  CUtensorMap in_w, in_x, out_w, out_h, out_h8;
   if (!weight_map(&in_w, enc, w.w_in, w.n_experts, w.dim, 2 * (int64_t)w.hidden) ||
-      !row_map(&in_x, enc, x, n_tokens, w.dim) || !weight_map(&out_w, enc, w.w_out, w.n_experts, w.hidden, w.dim) ||
-      !row_map(&out_h, enc, base + L.h, n_slots, w.hidden))
+      !row_map(&in_x, enc, x, n_tokens, w.dim, 1) || !weight_map(&out_w, enc, w.w_out, w.n_experts, w.hidden, w.dim) ||
+      !row_map(&out_h, enc, base + L.h, n_slots, w.hidden, 32) ||
+      !row_map(&out_h8, enc, base + L.h, n_slots, w.hidden, 8))
     return cudaErrorInvalidValue;
   const bool few = n_slots <= 16 * (int64_t)w.n_experts;
   const int tile_tokens = few ? 32 : 256;
   const int64_t max_tiles = n_slots / tile_tokens + (n_slots < w.n_experts ? n_slots : w.n_experts);
   static std::atomic<bool> attr[256];
-  cudaError_t e = set_smem_attr_once(experts_plan_kernel, 33 * 1024 * 4, attr);
+  cudaError_t e = set_smem_attr_once(experts_plan_kernel, 34 * 1024 * 4, attr);
   if (e != cudaSuccess) return e;
-  experts_plan_kernel<<<1, kPlanThreads, (size_t)33 * w.n_experts * 4, stream>>>(ids, n_slots, slots, w.n_experts,
-                                                                                 tile_tokens, plan, err);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  {
+    const unsigned blocks = n_slots > 1024 ? 8 : 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(blocks);
+    cfg.blockDim = dim3(kPlanThreads);
+    cfg.dynamicSmemBytes = (size_t)34 * w.n_experts * 4;
+    cfg.stream = stream;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = blocks;
+    at[0].val.clusterDim.y = 1;
+    at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, experts_plan_kernel, ids, n_slots, slots, w.n_experts, tile_tokens, plan, err);
+    if (e != cudaSuccess) return e;
+  }
   ++*launches;
   void *h = base + L.h, *y = base + L.y;
   auto products = [&](auto in, auto down) {
-    cudaError_t s = in(in_w, in_x, plan.n_tiles, plan.tiles, plan.token, w.dim, w.hidden, h, max_tiles, err, num_sms, stream);
+    cudaError_t s = in(in_w, in_x, in_x, plan.n_tiles, plan.tiles, plan.token, w.dim, w.hidden, h, max_tiles, err, num_sms, stream);
     if (s != cudaSuccess) return s;
     ++*launches;
-    s = down(out_w, out_h, plan.n_tiles, plan.tiles, plan.token, w.hidden, w.dim, y, max_tiles, err, num_sms, stream);
+    s = down(out_w, out_h, out_h8, plan.n_tiles, plan.tiles, plan.token, w.hidden, w.dim, y, max_tiles, err, num_sms, stream);
     if (s == cudaSuccess) ++*launches;
     return s;
   };
@@ -517,9 +620,18 @@ cudaError_t launch_experts(const void *x, int64_t n_tokens, const int32_t *ids, 
           : products(launch_product<256, true>, launch_product<256, false>);
   if (e != cudaSuccess) return e;
   const int64_t blocks = (n_tokens * (w.dim / 8) + 255) / 256, cap = (int64_t)num_sms * 32;
-  experts_sum_kernel<<<(unsigned)(blocks < cap ? blocks : cap), 256, 0, stream>>>(
-      static_cast<const float *>(y), plan.row, weights, n_tokens, slots, w.dim, static_cast<__nv_bfloat16 *>(out));
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(blocks < cap ? blocks : cap));
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  if ((e = cudaLaunchKernelEx(&cfg, experts_sum_kernel, static_cast<const float *>(y), (const int *)plan.row, weights,
+                              n_tokens, slots, (int)w.dim, static_cast<__nv_bfloat16 *>(out))) != cudaSuccess)
+    return e;
   ++*launches;
   return cudaSuccess;
 }
