@@ -2,9 +2,18 @@
 // router over 256 routed experts with 6 chosen per token, 2 shared experts always, and a joint
 // normalisation over the chosen and the shared).
 //
-// One warp per token: lane l holds the logits of experts l, l + 32, ... in registers, so a row is
-// read once, coalesced, and no value leaves the warp before the ids and weights are written. The
-// choice is top_k rounds of a warp-wide maximum over (value, lower index).
+// One warp per token: lane l holds experts l, l + 32, ... in registers, so a row is read once,
+// coalesced, and no value leaves the warp before the ids and weights are written. With many tokens
+// the kernel is bound by its instructions (about 850 per token of 256 experts, 72 % of the issue slots), not by the row's
+// 1 KB: each lane orders its experts by a network of comparisons on values whose last bits give way
+// to the expert's place, and top_k rounds take the largest head of the 32 lanes with one reduction
+// each. (8 lanes per token with their best 16 merged, so that four tokens share the rounds, needs
+// more registers than fit beside enough warps: 48 us for 24,000 tokens where this takes 27.)
+//
+// The order is that of 64-bit arithmetic, although the scores are fp32 and cut short: each round
+// also checks that its winner is above the next by more than the two can be off. A token where it
+// is not (about one in five hundred of ordinary logits) is chosen again in fp64, which takes that warp
+// 4 to 8 us: without such tokens the same call takes 19 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math_constants.h>
@@ -16,153 +25,366 @@
 namespace dmel {
 namespace {
 
-constexpr int kWarps = 4;  // tokens per block
+constexpr int kWarps = 4;  // per block
 constexpr unsigned kAll = 0xffffffffu;
+constexpr float kNone = -__builtin_huge_valf();  // "not to be chosen"
 
 __device__ __forceinline__ float logit(const float *p) { return __ldg(p); }
 __device__ __forceinline__ float logit(const __nv_bfloat16 *p) { return __bfloat162float(*p); }
 
-// A logit as the choice sees it: NaN is -inf (never chosen), +inf the largest finite value.
-__device__ __forceinline__ float clean(float l) { return l == l ? fminf(l, 3.402823466e38f) : -CUDART_INF_F; }
+// A logit as the choice sees it: NaN is -inf (never chosen; fmaxf drops it), +inf the largest finite
+// value.
+__device__ __forceinline__ float clean(float l) { return fminf(fmaxf(l, kNone), 3.402823466e38f); }
 
-// Largest value of the warp and the lowest index that holds it (idx differs between lanes).
-__device__ __forceinline__ void warp_best(double &v, int &idx) {
+// What a kernel is given of a dmel_router, with the experts per group and 2^20 / that, rounded up
+// (e / per = e * inv_per >> 20 for e < 1024), and the shared memory per warp.
+struct Settings {
+  dmel_router r;
+  int per, inv_per, warp_doubles;
+};
+
+// A key: an fp32 value whose last bits give way to the place i of N (a power of two), such that equal
+// values put lower places first. Keys are compared as floats.
+template <int N>
+__device__ __forceinline__ float key_of(float v, int i) {
+  const uint32_t u = __float_as_uint(fminf(v, 3.402823466e38f) + 0.0f);  // (no infinity, no -0)
+  const uint32_t low = u >> 31 ? (uint32_t)i : (uint32_t)(N - 1 - i);
+  return v > kNone ? __uint_as_float((u & ~(uint32_t)(N - 1)) | low) : kNone;
+}
+template <int N>
+__device__ __forceinline__ int place_of(float k) {
+  const uint32_t u = __float_as_uint(k), low = u & (N - 1);
+  return (int)(u >> 31 ? low : N - 1 - low);
+}
+template <int N>
+__device__ __forceinline__ float value_of(float k) {  // cut towards -inf, by less than N units
+  const uint32_t u = __float_as_uint(k);
+  return __uint_as_float(u >> 31 ? u | (N - 1) : u & ~(uint32_t)(N - 1));
+}
+
+// Bounds on the fp32 scores' errors: a sigmoid's 6e-7 (exp and reciprocal of a few ulps), a
+// softmax's 2e-6 (the same, and a sum of up to 1,056 terms by pairs).
+constexpr float kSigmoidOff = 6e-7f, kSoftmaxOff = 2e-6f;
+
+// How far apart two choice values must be for their keys, a above b, to order them as 64-bit
+// arithmetic does: twice the score's error, the rounding of the sums with the bias, and what
+// key_of<N> may have cut off b. Logits (not scored) are off only by what is cut.
+template <int N>
+__device__ __forceinline__ float margin(bool scored, bool sigmoid, float a, float b) {
+  const float off = scored ? 2.0f * (sigmoid ? kSigmoidOff : kSoftmaxOff) : 0.0f;
+  return off + (N + 2) * 1.2e-7f * fmaxf(fabsf(a), fabsf(b));
+}
+
+// exp and 1 / x on the special-function unit (a few ulps, results below the normal range zero).
+__device__ __forceinline__ float fast_exp(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * 1.4426950408889634f));
+  return y;
+}
+__device__ __forceinline__ float fast_rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// The warp's largest value, in one instruction.
+__device__ __forceinline__ float warp_max(float v) {
+  float m;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
+  return m;
+}
+template <typename F>
+__device__ __forceinline__ F warp_sum(F v) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const double ov = __shfl_xor_sync(kAll, v, o);
-    const int oi = __shfl_xor_sync(kAll, idx, o);
-    if (ov > v || (ov == v && oi < idx)) { v = ov; idx = oi; }
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
+  return v;
+}
+
+// Descending order by a network of comparisons (Batcher's odd-even merge sort; N a power of two).
+template <int N>
+__device__ __forceinline__ void sort_down(float (&v)[N]) {
+#pragma unroll
+  for (int p = 1; p < N; p <<= 1) {
+#pragma unroll
+    for (int k = p; k > 0; k >>= 1) {
+#pragma unroll
+      for (int j = k % p; j + k < N; j += 2 * k) {
+#pragma unroll
+        for (int i = 0; i < k; ++i) {
+          if (i + j + k < N && (i + j) / (2 * p) == (i + j + k) / (2 * p)) {
+            const float a = v[i + j], b = v[i + j + k];
+            v[i + j] = fmaxf(a, b);
+            v[i + j + k] = fminf(a, b);
+          }
+        }
+      }
+    }
   }
 }
 
+// Sum by pairs: an error of log2 N roundings.
+template <int N>
+__device__ __forceinline__ float pair_sum(float (&v)[N]) {
+#pragma unroll
+  for (int k = N / 2; k > 0; k >>= 1) {
+#pragma unroll
+    for (int i = 0; i < k; ++i) v[i] += v[i + k];
+  }
+  return v[0];
+}
+
+// Lanes that walk a group together: a power of two, and up to 32 groups fit the warp.
+__device__ __forceinline__ int lanes_per_group(int groups) {
+  return groups > 16 ? 1 : groups > 8 ? 2 : groups > 4 ? 4 : groups > 2 ? 8 : 16;
+}
+
+// The groups kept, a bit each. A group is rated by the sum of its two largest values (one where
+// there is only one). The values lie in shared memory, group g's from v + g (per + lanes_per_group):
+// that far apart, the lanes that walk the groups use different banks. *worst, *best: the lowest
+// rating kept, the highest left out, in lane 0.
+template <typename F>
+__device__ __forceinline__ unsigned keep_groups(const F *v, const Settings &q, F *worst, F *best) {
+  const int groups = q.r.n_groups, lane = threadIdx.x & 31, share = lanes_per_group(groups), mine = lane / share;
+  F m1 = kNone, m2 = kNone;
+  if (mine < groups) {
+    const F *p = v + mine * (q.per + share);
+#pragma unroll 4
+    for (int j = lane & (share - 1); j < q.per; j += share) {
+      const F x = p[j];
+      m2 = max(m2, min(m1, x));
+      m1 = max(m1, x);
+    }
+  }
+  __syncwarp();
+  for (int o = share >> 1; o > 0; o >>= 1) {
+    const F o1 = __shfl_xor_sync(kAll, m1, o), o2 = __shfl_xor_sync(kAll, m2, o);
+    m2 = max(max(m2, o2), min(m1, o1));
+    m1 = max(m1, o1);
+  }
+  F rated = __shfl_sync(kAll, m2 > kNone ? m1 + m2 : m1, (lane * share) & 31);  // group `lane`'s
+  if (lane >= groups) rated = kNone;
+  int before = 0;
+  for (int h = 0; h < groups; ++h) {
+    const F o = __shfl_sync(kAll, rated, h);
+    before += o > rated || (o == rated && h < lane);
+  }
+  const bool in = lane < groups && before < q.r.topk_groups;
+  F lo = in ? rated : -(F)kNone, hi = in ? (F)kNone : rated;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    lo = min(lo, __shfl_xor_sync(kAll, lo, o));
+    hi = max(hi, __shfl_xor_sync(kAll, hi, o));
+  }
+  *worst = lo;
+  *best = hi;
+  return __ballot_sync(kAll, in);
+}
+
+// A double as an unsigned number of the same order.
+__device__ __forceinline__ unsigned long long order_of(double v) {
+  const unsigned long long u = (unsigned long long)__double_as_longlong(v + 0.0);
+  return u >> 63 ? ~u : u | (1ull << 63);
+}
+
+// The choice in fp64: the id of slot `lane`, -1 for none. `top` is the token's largest logit, v the
+// warp's shared memory. Apart from the kernel, since one token in hundreds comes here; written for
+// a short way through, since the last of them ends the launch.
 template <typename T, int EPL>
-__global__ void __launch_bounds__(32 * kWarps) route_kernel(const T *__restrict__ logits, int64_t n_tokens,
-                                                            const float *__restrict__ bias, dmel_router r,
-                                                            int32_t *__restrict__ ids, float *__restrict__ weights) {
-  const int lane = threadIdx.x & 31;
-  const int E = r.n_experts, S = r.n_shared, K = r.top_k;
-  const int cols = E + S, slots = K + S;
-  extern __shared__ double group_smem[];  // [kWarps][E] choice values, with groups
-  const int64_t warps = (int64_t)gridDim.x * kWarps;
-  for (int64_t t = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5); t < n_tokens; t += warps) {
-    const T *row = logits + t * cols;
-    float l[EPL];
-    float top = -CUDART_INF_F;
-#pragma unroll
+__device__ __noinline__ int choose_fp64(const T *row, const float *bias, const Settings &q, float top, double *v) {
+  const dmel_router &r = q.r;
+  const int lane = threadIdx.x & 31, E = r.n_experts;
+  const bool softmax = r.scoring == DMEL_ROUTE_SOFTMAX;
+  constexpr int STEP = EPL < 8 ? EPL : 8;
+  double c[EPL], z = 0.0;
+#pragma unroll STEP
+  for (int i = 0; i < EPL; ++i) {
+    const int e = lane + 32 * i;
+    const double l = e < E ? (double)clean(logit(row + e)) : kNone;
+    c[i] = l;
+    if (bias || r.n_groups > 1) {
+      const double x = exp(softmax ? l - (double)top : -l);
+      c[i] = softmax ? x : 1.0 / (1.0 + x);
+      z += x;
+    }
+  }
+  if (bias || r.n_groups > 1) {
+    if (softmax) {
+      for (int e = E + lane; e < E + r.n_shared; e += 32) z += exp((double)clean(logit(row + e)) - (double)top);
+      z = 1.0 / warp_sum(z);
+    }
+#pragma unroll STEP
     for (int i = 0; i < EPL; ++i) {
       const int e = lane + 32 * i;
-      l[i] = e < E ? clean(logit(row + e)) : -CUDART_INF_F;
-      top = fmaxf(top, l[i]);
+      double x = softmax ? c[i] * z : c[i];
+      if (bias && e < E) x += (double)__ldg(bias + e);
+      c[i] = e < E && clean(logit(row + e)) > kNone && x == x ? x : (double)kNone;
     }
-    const float ls = lane < S ? clean(logit(row + E + lane)) : -CUDART_INF_F;  // shared expert `lane`
-    top = fmaxf(top, ls);
-    double z = 0.0;  // softmax: sum of exp(l - top) over every logit of the token
-    if (r.scoring == DMEL_ROUTE_SOFTMAX) {
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
-      if (top > -CUDART_INF_F) {
-#pragma unroll
-        for (int i = 0; i < EPL; ++i) z += exp((double)l[i] - top);
-        z += exp((double)ls - top);
-      }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(kAll, z, o);
-    }
-    auto score = [&](float x) -> double {
-      if (!(x > -CUDART_INF_F)) return 0.0;
-      return r.scoring == DMEL_ROUTE_SIGMOID ? 1.0 / (1.0 + exp(-(double)x)) : exp((double)x - top) / z;
-    };
-    // c[i]: what the choice compares. Without a bias the scores rise with the logits, so the
-    // logits themselves are compared (exactly); the groups' ratings need the scores.
-    double c[EPL];
-#pragma unroll
+  }
+  if (r.n_groups > 1) {
+    const int share = lanes_per_group(r.n_groups);
+#pragma unroll STEP
+    for (int i = 0; i < EPL; ++i)
+      if (lane + 32 * i < E) v[lane + 32 * i + (((lane + 32 * i) * q.inv_per) >> 20) * share] = c[i];
+    __syncwarp();
+    double worst, best;
+    const unsigned kept = keep_groups(v, q, &worst, &best);
+#pragma unroll STEP
     for (int i = 0; i < EPL; ++i) {
       const int e = lane + 32 * i;
-      const float b = bias && e < E ? __ldg(bias + e) : 0.0f;
-      c[i] = l[i] > -CUDART_INF_F && b == b ? (bias || r.n_groups > 1 ? score(l[i]) + (double)b : (double)l[i])
-                                            : -CUDART_INF;
+      if (!((kept >> ((e * q.inv_per) >> 20)) & 1u)) c[i] = kNone;
+      else if (!bias && c[i] > kNone) c[i] = (double)clean(logit(row + e));
     }
-    if (r.n_groups > 1) {
-      const int per = E / r.n_groups;
-      double *cs = group_smem + (threadIdx.x >> 5) * E;
+  }
+  int my_id = -1;
+  for (int k = 0; k < r.top_k; ++k) {
+    double m = kNone;
+    int at = 0;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i)
+      if (c[i] > m) { m = c[i]; at = i; }
+    // the largest of the warp, its high word first, then the lowest index among equals
+    const unsigned long long u = order_of(m);
+    const uint32_t hi = __reduce_max_sync(kAll, (uint32_t)(u >> 32));
+    const uint32_t lo = __reduce_max_sync(kAll, (uint32_t)(u >> 32) == hi ? (uint32_t)u : 0u);
+    const bool held = u == ((unsigned long long)hi << 32 | lo);
+    const int idx = (int)__reduce_min_sync(kAll, held && m > kNone ? (uint32_t)(lane + 32 * at) : 0x7fffffffu);
+    if (idx == 0x7fffffff) break;  // nothing left
+    if (lane == k) my_id = idx;
+    if (lane == (idx & 31)) {
 #pragma unroll
       for (int i = 0; i < EPL; ++i)
-        if (lane + 32 * i < E) cs[lane + 32 * i] = c[i];
-      __syncwarp();
-      double rated = -CUDART_INF;
-      if (lane < r.n_groups) {
-        double m1 = -CUDART_INF, m2 = -CUDART_INF;
-        for (int j = 0; j < per; ++j) {
-          const double v = cs[lane * per + j];
-          if (v > m1) { m2 = m1; m1 = v; } else if (v > m2) { m2 = v; }
-        }
-        rated = m2 > -CUDART_INF ? m1 + m2 : m1;
+        if (i == idx >> 5) c[i] = kNone;
+    }
+  }
+  return my_id;
+}
+
+// kScored: the choice compares scores (a bias, or groups), else the logits themselves.
+template <typename T, int EPL, bool kScored, bool kGroups>
+__global__ void __launch_bounds__(32 * kWarps) route_kernel(const T *__restrict__ logits, int64_t n_tokens,
+                                                            const float *__restrict__ bias, const Settings q,
+                                                            int32_t *__restrict__ ids, float *__restrict__ weights) {
+  const dmel_router &r = q.r;
+  const int lane = threadIdx.x & 31, E = r.n_experts, S = r.n_shared, K = r.top_k;
+  const int cols = E + S, slots = K + S;
+  const bool sigmoid = r.scoring == DMEL_ROUTE_SIGMOID;
+  extern __shared__ double smem[];  // with groups: a token's values per warp
+  double *const wide = smem + (threadIdx.x >> 5) * q.warp_doubles;
+  const int64_t step = (int64_t)gridDim.x * kWarps;
+  for (int64_t t = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5); t < n_tokens; t += step) {
+    const T *row = logits + t * cols;
+    auto at = [&](int e) { return clean(logit(row + e)); };
+    float l[EPL];
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) l[i] = lane + 32 * i < E ? logit(row + lane + 32 * i) : kNone;
+    const float ls = lane < S ? at(E + lane) : kNone;  // shared expert `lane`
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) l[i] = clean(l[i]);
+    float top = 0.0f, z = 1.0f;  // softmax: the largest logit, and the sum of exp(l - top)
+    if (!sigmoid) {
+      top = ls;
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) top = fmaxf(top, l[i]);
+      top = warp_max(top);
+      if (!(top > kNone)) top = 0.0f;
+      if (kScored || !r.renormalise) {
+        float x[EPL];
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) x[i] = fast_exp(l[i] - top);
+        z = warp_sum(pair_sum<EPL>(x) + fast_exp(ls - top));
       }
-      __syncwarp();
-      int before = 0;  // groups better than this lane's
-      for (int g = 0; g < r.n_groups; ++g) {
-        const double o = __shfl_sync(kAll, rated, g);
-        before += o > rated || (o == rated && g < lane);
+    }
+    // what the choice compares, -inf for what is not to be chosen
+    bool unsure = false;
+    float v[EPL];
+    if (kScored) {
+      const float inv_z = fast_rcp(z);
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) {
+        const float s = sigmoid ? fast_rcp(1.0f + fast_exp(-l[i])) : fast_exp(l[i] - top) * inv_z;
+        v[i] = l[i] > kNone ? s : kNone;
       }
-      const unsigned kept = __ballot_sync(kAll, lane < r.n_groups && before < r.topk_groups);
+      if (bias) {
+#pragma unroll
+        for (int i = 0; i < EPL; ++i)
+          if (lane + 32 * i < E) v[i] += __ldg(bias + lane + 32 * i);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) v[i] = l[i];
+    }
+    if (kGroups) {
+      float *const narrow = reinterpret_cast<float *>(wide);
+      const int share = lanes_per_group(r.n_groups);
 #pragma unroll
       for (int i = 0; i < EPL; ++i) {
         const int e = lane + 32 * i;
-        if (e < E && !((kept >> (e / per)) & 1u)) c[i] = -CUDART_INF;
-        else if (!bias && c[i] > -CUDART_INF) c[i] = (double)l[i];
+        if (e < E) narrow[e + ((e * q.inv_per) >> 20) * share] = fmaxf(v[i], kNone);  // (NaN: -inf)
+      }
+      __syncwarp();
+      float worst, best;
+      const unsigned kept = keep_groups(narrow, q, &worst, &best);
+      // two scores per rating, of which a softmax's are at most 1 together
+      unsure = best > kNone && !(worst - best > (sigmoid ? 2.0f : 1.0f) * margin<1>(true, sigmoid, worst, best));
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) {
+        const float x = bias ? v[i] : l[i];
+        v[i] = (kept >> (((lane + 32 * i) * q.inv_per) >> 20)) & 1u ? x : kNone;
+      }
+      __syncwarp();  // (read before the next token's values are written)
+    }
+    float key[EPL];
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) key[i] = key_of<EPL>(v[i], i);
+    sort_down<EPL>(key);
+    int my_id = -1;  // of slot `lane`
+    int last = 0;
+    float last_v = 0.0f;
+    for (int k = 0; k <= K; ++k) {  // the round after the last only checks the margin
+      const float best = warp_max(key[0]);
+      if (!(best > kNone)) break;  // nothing left
+      const int owner = __ffs(__ballot_sync(kAll, key[0] == best)) - 1;
+      const int idx = owner + 32 * place_of<EPL>(best);
+      const float b = value_of<EPL>(best);
+      if (lane == k) my_id = idx;
+      // nearer than they may be off; two experts alike are a tie, which goes by index here as well
+      if (k > 0 && !(last_v - b > margin<EPL>(bias != nullptr, sigmoid, last_v, b)) &&
+          !(at(last) == at(idx) && (!bias || __ldg(bias + last) == __ldg(bias + idx))))
+        unsure = true;
+      last = idx;
+      last_v = b;
+      if (lane == owner) {
+#pragma unroll
+        for (int i = 0; i + 1 < EPL; ++i) key[i] = key[i + 1];
+        key[EPL - 1] = kNone;
       }
     }
-    int my_id = -1;                 // slot `lane`
-    float my_l = -CUDART_INF_F;
-    for (int k = 0; k < K; ++k) {
-      double v = -CUDART_INF;
-      int idx = INT32_MAX;
-      float lv = -CUDART_INF_F;
-#pragma unroll
-      for (int i = 0; i < EPL; ++i)
-        if (c[i] > v) { v = c[i]; idx = lane + 32 * i; lv = l[i]; }
-      const int mine = idx;
-      warp_best(v, idx);
-      if (!(v > -CUDART_INF)) break;  // nothing left (the same in every lane)
-      const int owner = idx & 31;
-      const float won = __shfl_sync(kAll, lv, owner);
-      if (lane == owner && mine == idx) {
-#pragma unroll
-        for (int i = 0; i < EPL; ++i)
-          if (lane + 32 * i == idx) c[i] = -CUDART_INF;
-      }
-      if (lane == k) { my_id = idx; my_l = won; }
-    }
-    {  // shared experts in slots K .. K + S - 1
-      const float sl = __shfl_sync(kAll, ls, lane >= K ? lane - K : 0);
-      if (lane >= K && lane < slots && sl > -CUDART_INF_F) {
+    if (unsure) my_id = choose_fp64<T, EPL>(row, bias, q, top, wide);
+    float x = lane < K && my_id >= 0 ? at(my_id) : kNone;  // slot `lane`'s logit
+    if (lane >= K) my_id = -1;
+    if (S > 0) {  // shared experts in slots K .. K + S - 1
+      const float s = __shfl_sync(kAll, ls, (lane - K) & 31);
+      if (lane >= K && lane < slots && s > kNone) {
         my_id = E + lane - K;
-        my_l = sl;
+        x = s;
       }
     }
-    double wgt = my_id >= 0 ? score(my_l) : 0.0;
+    // weights. Renormalised: s / sum(s) from values scaled by exp(-m), m the largest chosen logit
+    // (sigmoid: where it is negative), so that scores too small for a float keep their ratios.
+    float m = sigmoid ? 0.0f : top;
     if (r.renormalise) {
-      // s / sum(s) from values scaled by exp(-m), m the largest chosen logit (sigmoid: where it is
-      // negative), so that scores too small for a float keep their ratios
-      float m = my_l;
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, o));
-      if (my_id >= 0) {
-        if (r.scoring == DMEL_ROUTE_SOFTMAX) {
-          wgt = exp((double)my_l - m);
-        } else {
-          const double shift = m < 0.0f ? (double)m : 0.0;
-          wgt = (my_l > 0.0f ? 1.0 : exp((double)my_l - shift)) / (1.0 + exp(-fabs((double)my_l)));
-        }
-      }
-      double sum = wgt;
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
-      wgt = sum > 0.0 ? wgt / sum : 0.0;
+      m = warp_max(x);
+      if (sigmoid) m = fminf(m, 0.0f);
     }
+    float w = 0.0f;
+    if (x > kNone) {
+      w = expf(sigmoid ? fminf(x, 0.0f) - m : x - m);
+      if (sigmoid) w = __fdividef(w, 1.0f + expf(-fabsf(x)));
+    }
+    if (r.renormalise) z = warp_sum(w);
     if (lane < slots) {
       ids[t * slots + lane] = my_id;
-      weights[t * slots + lane] = (float)(wgt * (double)r.scale);
+      weights[t * slots + lane] = z > 0.0f ? w / z * r.scale : 0.0f;
     }
   }
 }
@@ -170,17 +392,24 @@ __global__ void __launch_bounds__(32 * kWarps) route_kernel(const T *__restrict_
 template <typename T>
 cudaError_t launch_typed(const void *logits, int64_t n_tokens, const float *bias, const dmel_router &r, int32_t *ids,
                          float *weights, int num_sms, cudaStream_t stream) {
+  const int E = r.n_experts;
+  Settings q;
+  q.r = r;
+  q.per = E / r.n_groups;
+  q.inv_per = ((1 << 20) + q.per - 1) / q.per;
+  q.warp_doubles = r.n_groups > 1 ? E + 32 : 0;  // groups and the lanes per group: at most 32 together
+  const T *lt = static_cast<const T *>(logits);
+  const size_t smem = (size_t)kWarps * q.warp_doubles * sizeof(double);
   const int64_t blocks = (n_tokens + kWarps - 1) / kWarps, cap = (int64_t)num_sms * 64;
   const unsigned grid = (unsigned)(blocks < cap ? blocks : cap);
-  const size_t smem = r.n_groups > 1 ? (size_t)kWarps * r.n_experts * 8 : 0;
-  const T *lt = static_cast<const T *>(logits);
-#define DMEL_ROUTE(EPL) route_kernel<T, EPL><<<grid, 32 * kWarps, smem, stream>>>(lt, n_tokens, bias, r, ids, weights)
-  const int epl = (r.n_experts + 31) / 32;
-  if (epl <= 1) DMEL_ROUTE(1);
-  else if (epl <= 2) DMEL_ROUTE(2);
-  else if (epl <= 4) DMEL_ROUTE(4);
-  else if (epl <= 8) DMEL_ROUTE(8);
-  else if (epl <= 16) DMEL_ROUTE(16);
+#define DMEL_ROUTE(EPL)                                                                                             \
+  (r.n_groups > 1                                                                                                   \
+       ? route_kernel<T, EPL, true, true><<<grid, 32 * kWarps, smem, stream>>>(lt, n_tokens, bias, q, ids, weights) \
+   : bias                                                                                                           \
+       ? route_kernel<T, EPL, true, false><<<grid, 32 * kWarps, 0, stream>>>(lt, n_tokens, bias, q, ids, weights)   \
+       : route_kernel<T, EPL, false, false><<<grid, 32 * kWarps, 0, stream>>>(lt, n_tokens, bias, q, ids, weights))
+  if (E <= 64) DMEL_ROUTE(2);
+  else if (E <= 256) DMEL_ROUTE(8);
   else DMEL_ROUTE(32);
 #undef DMEL_ROUTE
   return cudaGetLastError();
