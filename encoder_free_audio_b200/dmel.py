@@ -164,9 +164,10 @@ def _stream(stream):
 
 def _dtype_code(t):
     import torch
-    if t.dtype == torch.float32:
+    dtype = t.dtype
+    if dtype == torch.float32:
         return DMEL_F32
-    if t.dtype == torch.bfloat16:
+    if dtype == torch.bfloat16:
         return DMEL_BF16
     raise TypeError(f"unsupported dtype {t.dtype}")
 
@@ -398,29 +399,35 @@ def _refuse(where: str, what: str):
     raise DmelError(DMEL_ERR_INVALID_ARG, f"{where} ({what})")
 
 
-def _addr(t, where: str, name: str, dtype, shape, device):
-    """The address of tensor t, which must have this type, shape and device and no gaps."""
-    if t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous():
-        _refuse(where, f"{name}: want a contiguous {dtype} tensor {tuple(shape)} on {device}, got {t.dtype} "
-                       f"{tuple(t.shape)} on {t.device} with strides {tuple(t.stride())}")
-    return t.data_ptr()
+def _addr(t, where: str, name: str, dtype, shape, device: int):
+    """The address of tensor t, which must have this type, shape and device index and no gaps."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == device and t.is_contiguous():
+        return t.data_ptr()
+    _refuse(where, f"{name}: want a contiguous {dtype} tensor {tuple(shape)} on {_device_name(device)}, got {t.dtype} "
+                   f"{tuple(t.shape)} on {t.device} with strides {tuple(t.stride())}")
 
 
-def _run_on(device, stream, where: str, entry, *args):
-    """entry(*args, stream) on `device`: on the given stream, or on the device's current one."""
+def _device_name(index: int) -> str:
+    return "the CPU" if index < 0 else f"cuda:{index}"
+
+
+def _run_on(device: int, stream, where: str, entry, *args):
+    """entry(*args, stream) on device number `device`: on the given stream, or on its current one."""
     import torch
-    if device.type != "cuda":
-        _refuse(where, f"tensors on {device}, want a CUDA device")
-    if stream is not None and stream.device != device:
-        _refuse(where, f"a stream of {stream.device} for tensors on {device}")
-    if device.index == torch.cuda.current_device():
-        raw = torch.cuda.current_stream(device).cuda_stream if stream is None else stream.cuda_stream
+    if device < 0:
+        _refuse(where, "tensors on the CPU, want a CUDA device")
+    if stream is None:  # (the number alone: a Stream object costs a microsecond)
+        raw = torch._C._cuda_getCurrentRawStream(device)
+    elif stream.device_index == device:
+        raw = stream.cuda_stream
+    else:
+        _refuse(where, f"a stream of {stream.device} for tensors on {_device_name(device)}")
+    if torch._C._cuda_getDevice() == device:
         rc = entry(*args, raw)
     else:
         with torch.cuda.device(device):
-            raw = torch.cuda.current_stream(device).cuda_stream if stream is None else stream.cuda_stream
             rc = entry(*args, raw)
-    if rc != DMEL_OK:
+    if rc:
         raise DmelError(rc, where)
 
 
@@ -431,20 +438,21 @@ def dmel_add_rmsnorm(x, rms_weight, out, residual=None, residual_out=None, eps: 
     scales fp32 [n, ceil(D / scale_block)] ([n, 1] or [n] for scale_block 0, one scale per row)."""
     import torch
     where = "dmel_add_rmsnorm"
-    if x.dim() != 2:
-        _refuse(where, f"x: want [rows, dim], got {tuple(x.shape)}")
-    shape, dt, dev = x.shape, x.dtype, x.device
+    shape, dt, dev = x.shape, x.dtype, x.get_device()
+    if len(shape) != 2:
+        _refuse(where, f"x: want [rows, dim], got {tuple(shape)}")
     n, d = shape
-    odt = DMEL_E4M3 if out.dtype is torch.float8_e4m3fn else _dtype_code(out)
+    code, odt = _dtype_code(x), out.dtype
     sc = None
     if scales is not None:
         blocks = -(-d // scale_block) if scale_block > 0 else 1
         sc = _addr(scales, where, "scales", torch.float32, (n,) if scales.dim() == 1 and blocks == 1 else (n, blocks), dev)
     _run_on(dev, stream, where, _lib().dmel_add_rmsnorm, _addr(x, where, "x", dt, shape, dev),
-            None if residual is None else _addr(residual, where, "residual", dt, shape, dev), n, d, _dtype_code(x),
+            None if residual is None else _addr(residual, where, "residual", dt, shape, dev), n, d, code,
             _addr(rms_weight, where, "rms_weight", dt, (d,), dev), eps,
             None if residual_out is None else _addr(residual_out, where, "residual_out", dt, shape, dev),
-            _addr(out, where, "out", out.dtype, shape, dev), odt, sc, scale_block)
+            _addr(out, where, "out", odt, shape, dev),
+            code if odt is dt else DMEL_E4M3 if odt is torch.float8_e4m3fn else _dtype_code(out), sc, scale_block)
 
 
 def dmel_route(logits, ids, weights, n_shared: int = 0, bias=None, scoring: int = DMEL_ROUTE_SIGMOID, n_groups: int = 1,
@@ -455,7 +463,7 @@ def dmel_route(logits, ids, weights, n_shared: int = 0, bias=None, scoring: int 
     where = "dmel_route"
     if logits.dim() != 2 or ids.dim() != 2:
         _refuse(where, f"logits and ids: want two dimensions, got {tuple(logits.shape)} and {tuple(ids.shape)}")
-    dev, n = logits.device, logits.shape[0]
+    dev, n = logits.get_device(), logits.shape[0]
     e, shape = logits.shape[1] - n_shared, (n, ids.shape[1])
     r = _router(e, n_shared, shape[1] - n_shared, n_groups, topk_groups, scoring, int(renormalise), scale)
     _run_on(dev, stream, where, _lib().dmel_route, _addr(logits, where, "logits", logits.dtype, logits.shape, dev), n,
@@ -477,7 +485,7 @@ def dmel_experts(x, ids, weights, w_in, w_out, out, workspace, stream=None):
     if x.dim() != 2 or ids.dim() != 2 or w_out.dim() != 3:
         _refuse(where, f"x, ids and w_out: want 2, 2 and 3 dimensions, got {tuple(x.shape)}, {tuple(ids.shape)} and "
                        f"{tuple(w_out.shape)}")
-    dev, bf16 = x.device, torch.bfloat16
+    dev, bf16 = x.get_device(), torch.bfloat16
     (n, d), (e, h, _), slots = x.shape, w_out.shape, ids.shape[1]
     w = ExpertWeights(e, d, h, _addr(w_in, where, "w_in", bf16, (e, d, 2 * h), dev),
                       _addr(w_out, where, "w_out", bf16, (e, h, d), dev))
