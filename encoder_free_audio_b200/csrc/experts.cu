@@ -180,6 +180,7 @@ struct EX {
   static constexpr int BOX = 64 * BK * 2;              // 64 columns x 64 K rows of weights: 8 KB
   static constexpr int A_STAGE = 2 * BOX;              // this CTA's 128 M rows
   static constexpr int B_STAGE = kTokens / 2 * BK * 2; // this CTA's half of the tokens
+  static constexpr int EPI_GROUPS = 2, EPI_WARPS = 4 * EPI_GROUPS;
   static constexpr int STG_TOKENS = 32;
   static constexpr int STG = STG_TOKENS * 128 * 4;     // 32 tokens x 128 columns, fp32
   static constexpr int IDX = kTokens / 2 * 4;          // row numbers of the half, for the gather warps
@@ -187,15 +188,16 @@ struct EX {
   static constexpr int STAGES = BUDGET / (A_STAGE + B_STAGE);
   static constexpr int OFF_B = STAGES * A_STAGE;
   static constexpr int OFF_STG = OFF_B + STAGES * B_STAGE;
-  static constexpr int OFF_BAR = OFF_STG + 2 * STG;
+  static constexpr int OFF_BAR = OFF_STG + EPI_GROUPS * STG;
   static constexpr int N_BARS = 2 * STAGES + 4 + 1;
   static constexpr int OFF_IDX = OFF_BAR + 512;
   static constexpr int SMEM_BYTES = OFF_IDX + IDX + 1024;
-  static constexpr int EPI_WARPS = 4;
-  // warp 0 TMA, warp 1 MMA, warps 2..5 epilogue, and for the gate and up products gather warps:
-  // one for narrow tiles, four for wide ones (4,096 tokens of 6 slots, 6144 x 2 x 1024: 971 us
-  // with two, 624 with four, 602 with plain boxes of rows in their place)
-  static constexpr int GATHER_WARPS = kTokens > 64 ? 4 : 1;
+  // warp 0 TMA, warp 1 MMA, warps 2..9 epilogue, and for the gate and up products gather warps. What
+  // bounds a gather of up to 128 rows per stage is how fast its loads are issued: 4,096 tokens of 6
+  // slots, 6144 x 2 x 1024: 780 us with two warps, 584 with four, 517 with eight (393 without any
+  // rows loaded). Copies by threads (16 bytes each) came to 1,350 us: the fence between them and the
+  // tensor cores takes about a microsecond per stage.
+  static constexpr int GATHER_WARPS = kTokens > 64 ? 8 : 2;
   static constexpr int THREADS = 32 * (2 + EPI_WARPS);
   static constexpr int THREADS_GATE = THREADS + 32 * GATHER_WARPS;
   static constexpr uint32_t ACC_STRIDE = kTokens;
@@ -204,6 +206,21 @@ struct EX {
   static_assert(B_STAGE % 1024 == 0 && STAGES >= 4 && STAGES <= 24, "stages");
   static_assert(N_BARS * 8 + 8 <= 512 && SMEM_BYTES <= 227 * 1024, "shared memory budget");
 };
+
+// Barrier of 128 threads by number; and one that also ANDs a flag, so that all take the same branch.
+__device__ __forceinline__ void group_bar(int id) { asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory"); }
+__device__ __forceinline__ bool group_bar_and(int id, bool v) {
+  uint32_t out;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "bar.red.and.pred q, %2, 128, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}\n"
+      : "=r"(out)
+      : "r"((uint32_t)v), "r"(id)
+      : "memory");
+  return out != 0;
+}
 
 __device__ __forceinline__ float4 silu_times(float4 g, float4 u) {
   // __expf and __fdividef are within a few fp32 ulps here; the result is rounded to bf16
@@ -384,25 +401,26 @@ __global__ void __launch_bounds__(kGate ? EX<kTokens>::THREADS_GATE : EX<kTokens
     }
   } else {
     // ------------------------------------------------ epilogue: lane = one M row (weight column)
-    const int quad = warp & 3, et = threadIdx.x - 64;
-    float *stg = reinterpret_cast<float *>(smem + X::OFF_STG);
-    uint32_t i = 0, n_chunk = 0;
+    // EPI_GROUPS groups of four warps (one per TMEM lane quarter) take chunks of 32 tokens in turn,
+    // each through a staging buffer of its own.
+    const int quad = warp & 3, group = (warp - 2) >> 2, et = (threadIdx.x - 64) & 127;
+    float *const buf = reinterpret_cast<float *>(smem + X::OFF_STG + group * X::STG);
+    uint32_t i = 0;
     bool ok = true;
     for (int64_t t = blockIdx.x >> 1; t < total; t += step, ++i) {
       const uint32_t acc = i & 1u, use = i >> 1;
       const TokenTile tt = tile_at(t);
       const int col = (int)(t % n_ct) * 2 * COLS + (int)rank * COLS;
-      ok = group_and<1, 32 * X::EPI_WARPS>(ok && mbar_wait(tfull(acc), use & 1u, err));
+      ok = group_bar_and(1 + group, ok && mbar_wait(tfull(acc), use & 1u, err));
       tc_fence_after();
       const uint32_t tb = tmem_base + ((uint32_t)(32 * quad) << 16) + acc * X::ACC_STRIDE;
-      for (int c = 0; ok && c < tt.width; c += X::STG_TOKENS, ++n_chunk) {
+      for (int c = X::STG_TOKENS * group; ok && c < tt.width; c += X::STG_TOKENS * X::EPI_GROUPS) {
         // 32 tokens (16 where the tile ends) of this lane's column into the staging rows
         const bool wide = tt.width - c >= 32;
         uint32_t v[2][16];
         tmem_ld16(tb + c, v[0]);
         if (wide) tmem_ld16(tb + c + 16, v[1]);
         tmem_wait_ld();
-        float *buf = stg + (n_chunk & 1u) * (X::STG / 4);
         const int m = 32 * quad + lane;
 #pragma unroll
         for (int k = 0; k < 16; ++k) buf[k * 128 + m] = __uint_as_float(v[0][k]);
@@ -410,30 +428,36 @@ __global__ void __launch_bounds__(kGate ? EX<kTokens>::THREADS_GATE : EX<kTokens
 #pragma unroll
           for (int k = 0; k < 16; ++k) buf[(16 + k) * 128 + m] = __uint_as_float(v[1][k]);
         }
-        // one barrier per chunk: the buffer of two chunks ago was read before the last barrier
-        asm volatile("bar.sync 1, 128;" ::: "memory");
+        group_bar(1 + group);
         const int n_tok = tt.rows - c < 32 ? tt.rows - c : 32;
         if (kGate) {
-          __nv_bfloat16 *h = static_cast<__nv_bfloat16 *>(out);
-          const int q = et & 15;  // 4 columns, a token per 16 threads
+          __nv_bfloat16 *h = static_cast<__nv_bfloat16 *>(out) + (int64_t)(tt.row0 + c) * cols + col;
+          const int q = et & 15, k0 = et >> 4;  // 4 columns, a token per 16 threads
           if (col + 4 * q < cols) {
-            for (int k = et >> 4; k < n_tok; k += 8) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int k = k0 + 8 * j;
               const float4 g = *reinterpret_cast<const float4 *>(buf + k * 128 + 4 * q);
               const float4 u = *reinterpret_cast<const float4 *>(buf + k * 128 + 64 + 4 * q);
               const float4 y = silu_times(g, u);
-              *reinterpret_cast<uint2 *>(h + (int64_t)(tt.row0 + c + k) * cols + col + 4 * q) =
-                  make_uint2(pack_bf16(y.x, y.y), pack_bf16(y.z, y.w));
+              if (k < n_tok)
+                *reinterpret_cast<uint2 *>(h + (int64_t)k * cols + 4 * q) =
+                    make_uint2(pack_bf16(y.x, y.y), pack_bf16(y.z, y.w));
             }
           }
         } else {
-          float *y = static_cast<float *>(out);
-          const int q = et & 31;  // 4 columns, a token per warp
+          float *y = static_cast<float *>(out) + (int64_t)(tt.row0 + c) * cols + col;
+          const int q = et & 31, k0 = et >> 5;  // 4 columns, a token per warp
           if (col + 4 * q < cols) {
-            for (int k = et >> 5; k < n_tok; k += 4)
-              *reinterpret_cast<float4 *>(y + (int64_t)(tt.row0 + c + k) * cols + col + 4 * q) =
-                  *reinterpret_cast<const float4 *>(buf + k * 128 + 4 * q);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const int k = k0 + 4 * j;
+              const float4 r = *reinterpret_cast<const float4 *>(buf + k * 128 + 4 * q);
+              if (k < n_tok) *reinterpret_cast<float4 *>(y + (int64_t)k * cols + 4 * q) = r;
+            }
           }
         }
+        group_bar(1 + group);  // the buffer has been read
       }
       tc_fence_before();
       __syncwarp();
