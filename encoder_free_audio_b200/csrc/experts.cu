@@ -2,8 +2,10 @@
 // Design", Part 3 · Inference: 256 routed and 2 shared experts, 6 chosen per token):
 //     out[t] = sum_j weights[t, j] (silu(x[t] G_e) * (x[t] U_e)) D_e,   e = ids[t, j].
 //
-// Four launches: a plan (the slots ordered by expert, cut into tiles of tokens), the gate and up
-// products with the gating in the epilogue, the down product, and each token's weighted sum.
+// Four steps: a plan (the slots ordered by expert, cut into tiles of tokens), the gate and up
+// products with the gating in the epilogue, the down product, and each token's weighted sum. Up to
+// kSmallSlots slots take two launches: every block of the first product makes the plan itself, and
+// the last block of the second to finish some columns sums them. More take one launch each.
 //
 // Both products run on the tensor cores with the roles swapped: an expert's weights are the M
 // side (256 weight columns per pair of CTAs) and its tokens the N side, whose size an MMA takes in
@@ -169,12 +171,91 @@ __global__ void __launch_bounds__(kPlanThreads) experts_plan_kernel(const int32_
   }
 }
 
+// The same for at most kSmallSlots slots, by every block of the first product for itself in shared
+// memory, by comparing each slot with all others. The `writer` block also leaves it in memory for
+// the second product, and clears its counters. With the sums in the second product that saves two
+// launches: one token's 6 slots 49.5 us against 53. With 384 slots both cost more than the launches
+// (277 us against 208: the comparisons, and a fence per tile).
+constexpr int kSmallSlots = 64;
+
+struct SmallPlan {
+  TokenTile tiles[kSmallSlots];
+  int token[kSmallSlots];
+  int n_tiles;
+};
+
+struct SmallCall {
+  const int32_t *ids;
+  const float *weights;
+  int n_slots, slots, n_experts, n_counters;
+  int *counters;        // per 128 columns of the output: token tiles done
+  __nv_bfloat16 *out;
+  PlanOut plan;
+};
+
+__device__ __forceinline__ void make_small_plan(const SmallCall &c, int tile_tokens, SmallPlan *p, int *expert,
+                                                int *starts, bool writer, uint32_t *err) {
+  const int n = c.n_slots;
+  for (int i = threadIdx.x; i < n; i += blockDim.x) {
+    const int e = c.ids[i];
+    const bool valid = e >= 0 && e < c.n_experts;
+    if (!valid && e != -1) record_error(err, DMEL_DEVERR_EXPERT);
+    expert[i] = valid ? e : INT32_MAX;
+  }
+  if (threadIdx.x == 0) p->n_tiles = 0;
+  __syncthreads();
+  for (int i = threadIdx.x; i < n; i += blockDim.x) {
+    const int e = expert[i];
+    int first = 0, count = 0, before = 0;  // slots of lower experts, of this one, of this one before i
+    for (int j = 0; j < n; ++j) {
+      const int o = expert[j];
+      first += o < e;
+      count += o == e;
+      before += o == e && j < i;
+    }
+    int rows = 0;  // of the tile that starts with this slot
+    if (e != INT32_MAX) {
+      const int tiles = (count + tile_tokens - 1) / tile_tokens, width = ((count + tiles - 1) / tiles + 15) / 16 * 16;
+      p->token[first + before] = i / c.slots;
+      if (before % width == 0) {
+        rows = count - before < width ? count - before : width;
+        atomicAdd(&p->n_tiles, 1);
+      }
+    }
+    starts[i] = rows;
+    if (writer) c.plan.row[i] = e != INT32_MAX ? first + before : -1;
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < n; i += blockDim.x) {
+    if (starts[i] == 0) continue;
+    const int e = expert[i];
+    int at = 0, row0 = 0;  // tiles before this one, and its first row
+    for (int j = 0; j < n; ++j) {
+      const bool earlier = expert[j] < e || (expert[j] == e && j < i);
+      row0 += earlier;
+      at += earlier && starts[j] != 0;
+    }
+    TokenTile t;
+    t.expert = e;
+    t.row0 = row0;
+    t.rows = starts[i];
+    t.width = (starts[i] + 15) / 16 * 16;
+    p->tiles[at] = t;
+    if (writer) c.plan.tiles[at] = t;
+  }
+  if (writer) {
+    for (int i = threadIdx.x; i < c.n_counters; i += blockDim.x) c.counters[i] = 0;
+    if (threadIdx.x == 0) *c.plan.n_tiles = p->n_tiles;
+  }
+  __syncthreads();
+}
+
 // ---------------------------------------------------------------- products (tcgen05, CTA pairs)
 //
 // kGate: D[columns x tokens] of both the gate's and the up product: each CTA's 128 M rows are 64 of
 // the gate's columns and the 64 up columns beside them, the epilogue writes bf16(silu(g) u) to
 // h [rows x hidden]. Otherwise: 128 columns of the down product per CTA, written as fp32 rows.
-template <int kTokens>
+template <int kTokens, bool kSmall = false>
 struct EX {
   static constexpr int BK = 64;                        // K per stage: 128 bytes of a token row
   static constexpr int BOX = 64 * BK * 2;              // 64 columns x 64 K rows of weights: 8 KB
@@ -184,14 +265,16 @@ struct EX {
   static constexpr int STG_TOKENS = 32;
   static constexpr int STG = STG_TOKENS * 128 * 4;     // 32 tokens x 128 columns, fp32
   static constexpr int IDX = kTokens / 2 * 4;          // row numbers of the half, for the gather warps
-  static constexpr int BUDGET = 227 * 1024 - 1024 - 512 - IDX - 2 * STG;
+  static constexpr int PLAN = kSmall ? (int)((sizeof(SmallPlan) + 15) / 16 * 16) : 0;
+  static constexpr int BUDGET = 227 * 1024 - 1024 - 512 - IDX - PLAN - EPI_GROUPS * STG;
   static constexpr int STAGES = BUDGET / (A_STAGE + B_STAGE);
   static constexpr int OFF_B = STAGES * A_STAGE;
   static constexpr int OFF_STG = OFF_B + STAGES * B_STAGE;
   static constexpr int OFF_BAR = OFF_STG + EPI_GROUPS * STG;
   static constexpr int N_BARS = 2 * STAGES + 4 + 1;
   static constexpr int OFF_IDX = OFF_BAR + 512;
-  static constexpr int SMEM_BYTES = OFF_IDX + IDX + 1024;
+  static constexpr int OFF_PLAN = OFF_IDX + IDX;
+  static constexpr int SMEM_BYTES = OFF_PLAN + PLAN + 1024;
   // warp 0 TMA, warp 1 MMA, warps 2..9 epilogue, and for the gate and up products gather warps. What
   // bounds a gather of up to 128 rows per stage is how fast its loads are issued: 4,096 tokens of 6
   // slots, 6144 x 2 x 1024: 780 us with two warps, 584 with four, 517 with eight (393 without any
@@ -228,13 +311,37 @@ __device__ __forceinline__ float4 silu_times(float4 g, float4 u) {
                      __fdividef(g.z, 1.0f + __expf(-g.z)) * u.z, __fdividef(g.w, 1.0f + __expf(-g.w)) * u.w);
 }
 
-template <int kTokens, bool kGate>
-__global__ void __launch_bounds__(kGate ? EX<kTokens>::THREADS_GATE : EX<kTokens>::THREADS, 1)
+// 128 columns from `col` on of every token's weighted sum, by the 256 epilogue threads: the rows y
+// (dim columns each, other blocks' work among them) in slot order.
+__device__ __forceinline__ void small_sum(const SmallCall &c, const float *y, int dim, int col) {
+  const int et = threadIdx.x - 64, q = col + 4 * (et & 31), n_tokens = c.n_slots / c.slots;
+  if (q >= dim) return;
+  for (int t = et >> 5; t < n_tokens; t += 8) {
+    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+    for (int j = 0; j < c.slots; ++j) {
+      const int r = __ldcg(c.plan.row + t * c.slots + j);
+      if (r < 0) continue;
+      const float w = c.weights[t * c.slots + j];
+      const float4 v = __ldcg(reinterpret_cast<const float4 *>(y + (int64_t)r * dim + q));
+      acc.x = fmaf(w, v.x, acc.x);
+      acc.y = fmaf(w, v.y, acc.y);
+      acc.z = fmaf(w, v.z, acc.z);
+      acc.w = fmaf(w, v.w, acc.w);
+    }
+    *reinterpret_cast<uint2 *>(c.out + (int64_t)t * dim + q) =
+        make_uint2(pack_bf16(acc.x, acc.y), pack_bf16(acc.z, acc.w));
+  }
+}
+
+// kSmall: the gate's kernel makes the plan, the down product's kernel the tokens' sums (SmallCall).
+template <int kTokens, bool kGate, bool kSmall>
+__global__ void __launch_bounds__(kGate ? EX<kTokens, kSmall>::THREADS_GATE : EX<kTokens, kSmall>::THREADS, 1)
     experts_product_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
                            const __grid_constant__ CUtensorMap xmap8, const int *__restrict__ n_tiles,
-                           const TokenTile *__restrict__ tiles, const int *__restrict__ token, int K, int cols,
-                           void *__restrict__ out, uint32_t *err) {
-  using X = EX<kTokens>;
+                           const TokenTile *tiles, const int *token, int K, int cols, void *out, const SmallCall small,
+                           uint32_t *err) {
+  using X = EX<kTokens, kSmall>;
   constexpr int STAGES = X::STAGES, BK = X::BK;
   constexpr int COLS = kGate ? 64 : 128;  // columns of the output per CTA
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -277,9 +384,20 @@ __global__ void __launch_bounds__(kGate ? EX<kTokens>::THREADS_GATE : EX<kTokens
   // (Letting the down product load its first weights before this wait measured the same.)
   wait_for_predecessors();
   launch_dependents();
+  int token_tiles;
+  if (kSmall && kGate) {
+    SmallPlan *p = reinterpret_cast<SmallPlan *>(smem + X::OFF_PLAN);
+    int *scratch = reinterpret_cast<int *>(smem + X::OFF_STG);  // (the epilogue's, not yet in use)
+    make_small_plan(small, kTokens, p, scratch, scratch + kSmallSlots, blockIdx.x == 0, err);
+    token_tiles = p->n_tiles;
+    tiles = p->tiles;
+    token = p->token;
+  } else {
+    token_tiles = *n_tiles;
+  }
 
   const int n_ct = (cols + 2 * COLS - 1) / (2 * COLS);  // column tiles
-  const int64_t total = (int64_t)*n_tiles * n_ct;
+  const int64_t total = (int64_t)token_tiles * n_ct;
   const int KB = (K + BK - 1) / BK;
   const int64_t step = gridDim.x >> 1;
   // consecutive pairs take the column tiles of one token tile (its rows stay in L2)
@@ -462,7 +580,23 @@ __global__ void __launch_bounds__(kGate ? EX<kTokens>::THREADS_GATE : EX<kTokens
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_remote(mapa_shared(tempty(acc), 0));
+      if (kSmall && !kGate) {
+        // the last block to finish these columns (in whatever order) sums them for every token
+        int *last = reinterpret_cast<int *>(smem + X::OFF_IDX);
+        __threadfence();
+        asm volatile("bar.sync 3, %0;" ::"n"(32 * X::EPI_WARPS) : "memory");
+        if (threadIdx.x == 64) {
+          __threadfence();
+          *last = atomicAdd(small.counters + 2 * (t % n_ct) + rank, 1) == token_tiles - 1;
+          __threadfence();
+        }
+        asm volatile("bar.sync 3, %0;" ::"n"(32 * X::EPI_WARPS) : "memory");
+        if (*last) small_sum(small, static_cast<const float *>(out), cols, col);
+      }
     }
+    if (kSmall && !kGate && token_tiles == 0)  // no token has an expert: zeros
+      for (int64_t ct = blockIdx.x >> 1; ct < n_ct; ct += step)
+        small_sum(small, static_cast<const float *>(out), cols, (int)ct * 2 * COLS + (int)rank * COLS);
   }
 
   tc_fence_before();
@@ -509,12 +643,13 @@ size_t r256(size_t x) { return (x + 255) / 256 * 256; }
 constexpr int kMinTile = 32;  // the narrowest token tile of the product kernels
 
 struct Layout {
-  size_t n_tiles, tiles, token, row, h, y, total;
+  size_t n_tiles, counters, tiles, token, row, h, y, total;
 };
 Layout layout(int64_t n_tokens, int slots, const dmel_expert_weights &w) {
   const size_t n = (size_t)n_tokens * slots;
   // one tile per started kMinTile tokens of an expert
   const size_t tiles = n / kMinTile + (n < (size_t)w.n_experts ? n : (size_t)w.n_experts);
+  // (counters: one per 128 columns of the output, in pairs)
   Layout L;
   size_t at = 0;
   auto take = [&](size_t bytes) {
@@ -523,6 +658,7 @@ Layout layout(int64_t n_tokens, int slots, const dmel_expert_weights &w) {
     return here;
   };
   L.n_tiles = take(4);
+  L.counters = take((size_t)(w.dim + 255) / 256 * 2 * 4);
   L.tiles = take(tiles * sizeof(TokenTile));
   L.token = take(n * 4);
   L.row = take(n * 4);
@@ -554,21 +690,32 @@ bool row_map(CUtensorMap *map, EncodeTiledFn enc, const void *base, int64_t R, i
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int kTokens, bool kGate>
-cudaError_t launch_product(const CUtensorMap &wmap, const CUtensorMap &xmap, const CUtensorMap &xmap8,
-                           const int *n_tiles, const TokenTile *tiles, const int *token, int K, int cols, void *out, int64_t max_tiles,
-                           uint32_t *err, int num_sms, cudaStream_t stream) {
-  using X = EX<kTokens>;
+// What the two products of a call need.
+struct Call {
+  CUtensorMap in_w, in_x, out_w, out_h, out_h8;
+  int dim, hidden;
+  void *h, *y;
+  SmallCall small;
+  int64_t max_tiles;
+  uint32_t *err;
+  int num_sms;
+  cudaStream_t stream;
+};
+
+template <int kTokens, bool kGate, bool kSmall>
+cudaError_t launch_product(const Call &c) {
+  using X = EX<kTokens, kSmall>;
   static std::atomic<bool> attr[256];
-  const cudaError_t e = set_smem_attr_once(experts_product_kernel<kTokens, kGate>, X::SMEM_BYTES, attr);
+  const auto kernel = experts_product_kernel<kTokens, kGate, kSmall>;
+  const cudaError_t e = set_smem_attr_once(kernel, X::SMEM_BYTES, attr);
   if (e != cudaSuccess) return e;
-  const int per_pair = kGate ? 128 : 256;
-  const int64_t work = max_tiles * ((cols + per_pair - 1) / per_pair), pairs = num_sms / 2 > 0 ? num_sms / 2 : 1;
+  const int cols = kGate ? c.hidden : c.dim, per_pair = kGate ? 128 : 256;
+  const int64_t work = c.max_tiles * ((cols + per_pair - 1) / per_pair), pairs = c.num_sms / 2 > 0 ? c.num_sms / 2 : 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(2 * (work < pairs ? work : pairs)));
   cfg.blockDim = dim3(kGate ? X::THREADS_GATE : X::THREADS);
   cfg.dynamicSmemBytes = X::SMEM_BYTES;
-  cfg.stream = stream;
+  cfg.stream = c.stream;
   cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeClusterDimension;
   at[0].val.clusterDim.x = 2;
@@ -577,9 +724,61 @@ cudaError_t launch_product(const CUtensorMap &wmap, const CUtensorMap &xmap, con
   at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
-  cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, experts_product_kernel<kTokens, kGate>, wmap, xmap, xmap8, n_tiles, tiles, token, K, cols,
-                            out, err);
+  cfg.numAttrs = kSmall && kGate ? 1 : 2;  // (the first launch of a call starts when all before it is done)
+  const PlanOut &p = c.small.plan;
+  return cudaLaunchKernelEx(&cfg, kernel, kGate ? c.in_w : c.out_w, kGate ? c.in_x : c.out_h, c.out_h8,
+                            (const int *)p.n_tiles, (const TokenTile *)p.tiles, (const int *)p.token,
+                            kGate ? c.dim : c.hidden, cols, kGate ? c.h : c.y, c.small, c.err);
+}
+
+template <int kTokens, bool kSmall>
+cudaError_t launch_products(const Call &c, int *launches) {
+  cudaError_t e = launch_product<kTokens, true, kSmall>(c);
+  if (e != cudaSuccess) return e;
+  ++*launches;
+  e = launch_product<kTokens, false, kSmall>(c);
+  if (e == cudaSuccess) ++*launches;
+  return e;
+}
+
+cudaError_t launch_plan(const Call &c, int tile_tokens, int *launches) {
+  static std::atomic<bool> attr[256];
+  cudaError_t e = set_smem_attr_once(experts_plan_kernel, 34 * 1024 * 4, attr);
+  if (e != cudaSuccess) return e;
+  const SmallCall &s = c.small;
+  const unsigned blocks = s.n_slots > 1024 ? 8 : 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(blocks);
+  cfg.blockDim = dim3(kPlanThreads);
+  cfg.dynamicSmemBytes = (size_t)34 * s.n_experts * 4;
+  cfg.stream = c.stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = blocks;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, experts_plan_kernel, s.ids, s.n_slots, s.slots, s.n_experts, tile_tokens, s.plan, c.err);
+  if (e == cudaSuccess) ++*launches;
+  return e;
+}
+
+cudaError_t launch_sum(const Call &c, int64_t n_tokens, int *launches) {
+  const int64_t blocks = (n_tokens * (c.dim / 8) + 255) / 256, cap = (int64_t)c.num_sms * 32;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(blocks < cap ? blocks : cap));
+  cfg.blockDim = dim3(256);
+  cfg.stream = c.stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, experts_sum_kernel, (const float *)c.y, (const int *)c.small.plan.row,
+                                           c.small.weights, n_tokens, c.small.slots, c.dim, c.small.out);
+  if (e == cudaSuccess) ++*launches;
+  return e;
 }
 
 }  // namespace
@@ -596,68 +795,40 @@ cudaError_t launch_experts(const void *x, int64_t n_tokens, const int32_t *ids, 
   const Layout L = layout(n_tokens, slots, w);
   uint8_t *base = static_cast<uint8_t *>(workspace);
   const int n_slots = (int)(n_tokens * slots);
-  PlanOut plan;
-  plan.n_tiles = reinterpret_cast<int *>(base + L.n_tiles);
-  plan.tiles = reinterpret_cast<TokenTile *>(base + L.tiles);
-  plan.token = reinterpret_cast<int *>(base + L.token);
-  plan.row = reinterpret_cast<int *>(base + L.row);
-  CUtensorMap in_w, in_x, out_w, out_h, out_h8;
-  if (!weight_map(&in_w, enc, w.w_in, w.n_experts, w.dim, 2 * (int64_t)w.hidden) ||
-      !row_map(&in_x, enc, x, n_tokens, w.dim, 1) || !weight_map(&out_w, enc, w.w_out, w.n_experts, w.hidden, w.dim) ||
-      !row_map(&out_h, enc, base + L.h, n_slots, w.hidden, 32) ||
-      !row_map(&out_h8, enc, base + L.h, n_slots, w.hidden, 8))
+  Call c;
+  c.dim = w.dim;
+  c.hidden = w.hidden;
+  c.h = base + L.h;
+  c.y = base + L.y;
+  c.err = err;
+  c.num_sms = num_sms;
+  c.stream = stream;
+  SmallCall &s = c.small;
+  s.ids = ids;
+  s.weights = weights;
+  s.n_slots = n_slots;
+  s.slots = slots;
+  s.n_experts = w.n_experts;
+  s.n_counters = (w.dim + 255) / 256 * 2;
+  s.counters = reinterpret_cast<int *>(base + L.counters);
+  s.out = static_cast<__nv_bfloat16 *>(out);
+  s.plan.n_tiles = reinterpret_cast<int *>(base + L.n_tiles);
+  s.plan.tiles = reinterpret_cast<TokenTile *>(base + L.tiles);
+  s.plan.token = reinterpret_cast<int *>(base + L.token);
+  s.plan.row = reinterpret_cast<int *>(base + L.row);
+  if (!weight_map(&c.in_w, enc, w.w_in, w.n_experts, w.dim, 2 * (int64_t)w.hidden) ||
+      !row_map(&c.in_x, enc, x, n_tokens, w.dim, 1) || !weight_map(&c.out_w, enc, w.w_out, w.n_experts, w.hidden, w.dim) ||
+      !row_map(&c.out_h, enc, c.h, n_slots, w.hidden, 32) || !row_map(&c.out_h8, enc, c.h, n_slots, w.hidden, 8))
     return cudaErrorInvalidValue;
-  const bool few = n_slots <= 16 * (int64_t)w.n_experts;
-  const int tile_tokens = few ? 32 : 256;
-  const int64_t max_tiles = n_slots / tile_tokens + (n_slots < w.n_experts ? n_slots : w.n_experts);
-  static std::atomic<bool> attr[256];
-  cudaError_t e = set_smem_attr_once(experts_plan_kernel, 34 * 1024 * 4, attr);
-  if (e != cudaSuccess) return e;
-  {
-    const unsigned blocks = n_slots > 1024 ? 8 : 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(blocks);
-    cfg.blockDim = dim3(kPlanThreads);
-    cfg.dynamicSmemBytes = (size_t)34 * w.n_experts * 4;
-    cfg.stream = stream;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = blocks;
-    at[0].val.clusterDim.y = 1;
-    at[0].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, experts_plan_kernel, ids, n_slots, slots, w.n_experts, tile_tokens, plan, err);
-    if (e != cudaSuccess) return e;
-  }
-  ++*launches;
-  void *h = base + L.h, *y = base + L.y;
-  auto products = [&](auto in, auto down) {
-    cudaError_t s = in(in_w, in_x, in_x, plan.n_tiles, plan.tiles, plan.token, w.dim, w.hidden, h, max_tiles, err, num_sms, stream);
-    if (s != cudaSuccess) return s;
-    ++*launches;
-    s = down(out_w, out_h, out_h8, plan.n_tiles, plan.tiles, plan.token, w.hidden, w.dim, y, max_tiles, err, num_sms, stream);
-    if (s == cudaSuccess) ++*launches;
-    return s;
-  };
-  e = few ? products(launch_product<32, true>, launch_product<32, false>)
-          : products(launch_product<256, true>, launch_product<256, false>);
-  if (e != cudaSuccess) return e;
-  const int64_t blocks = (n_tokens * (w.dim / 8) + 255) / 256, cap = (int64_t)num_sms * 32;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(blocks < cap ? blocks : cap));
-  cfg.blockDim = dim3(256);
-  cfg.stream = stream;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  if ((e = cudaLaunchKernelEx(&cfg, experts_sum_kernel, static_cast<const float *>(y), (const int *)plan.row, weights,
-                              n_tokens, slots, (int)w.dim, static_cast<__nv_bfloat16 *>(out))) != cudaSuccess)
-    return e;
-  ++*launches;
-  return cudaSuccess;
+  // Tiles of 32 tokens (ten stages of weights in flight) where an expert has 16 or fewer on average:
+  // the weights' bytes bound such calls; else wide ones, whose tokens share a pass over the weights.
+  const bool small = n_slots <= kSmallSlots, narrow = small || n_slots <= 16 * (int64_t)w.n_experts;
+  const int tile_tokens = narrow ? 32 : 256;
+  c.max_tiles = n_slots / tile_tokens + (n_slots < w.n_experts ? n_slots : w.n_experts);
+  if (small) return launch_products<32, true>(c, launches);
+  cudaError_t e = launch_plan(c, tile_tokens, launches);
+  if (e == cudaSuccess) e = narrow ? launch_products<32, false>(c, launches) : launch_products<256, false>(c, launches);
+  return e == cudaSuccess ? launch_sum(c, n_tokens, launches) : e;
 }
 
 }  // namespace dmel

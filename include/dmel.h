@@ -417,7 +417,7 @@ dmel_status dmel_route(const void *logits, int64_t n_tokens, dmel_dtype dtype, c
  * Products sum in fp32; the gated hidden row is rounded to bf16 once (the second product's
  * operand), each expert's output row stays fp32 until the token's sum, which is rounded to bf16.
  * Results do not depend on how tokens are batched, up to fp32 summation inside the tensor cores.
- * n_tokens * slots at most 2^30. Asynchronous on stream, four launches. */
+ * n_tokens * slots at most 2^30. Asynchronous on stream; two launches up to 64 slots, then four. */
 typedef struct {
   int n_experts;     /* 1 .. 1024 */
   int dim;           /* model width, a positive multiple of 8, at most 65536 */
