@@ -408,12 +408,13 @@ def route(logits: np.ndarray, n_shared: int, top_k: int, sigmoid: bool, bias=Non
 def experts(x: np.ndarray, ids: np.ndarray, weights: np.ndarray, w_in: np.ndarray, w_out: np.ndarray):
     """The experts' products in fp64, slot by slot: out[t] = sum_j weights[t, j] (silu(x G) * (x U)) D of
     expert ids[t, j]. Returns (out, h [T, slots, H], how far bf16 rounding of h and the fp32 sums (one
-    rounding of 2^-23 per 16 products) may move each output at most)."""
+    rounding of 2^-23 per 16 products) may move each output at most, the sum of the weighted slots'
+    magnitudes)."""
     x, w_in, w_out = (np.asarray(a, np.float64) for a in (x, w_in, w_out))
     T, slots = ids.shape
     H = w_out.shape[1]
     out = np.zeros((T, w_out.shape[2]))
-    spread = np.zeros_like(out)
+    spread, size = np.zeros_like(out), np.zeros_like(out)
     hidden = np.zeros((T, slots, H))
     for t in range(T):
         for j in range(slots):
@@ -425,12 +426,14 @@ def experts(x: np.ndarray, ids: np.ndarray, weights: np.ndarray, w_in: np.ndarra
             h = g / (1.0 + np.exp(-g)) * u
             b = np.abs(x[t]) @ np.abs(w_in[e])
             hidden[t, j] = h
-            out[t] += weights[t, j] * (h @ w_out[e])
+            y = weights[t, j] * (h @ w_out[e])
+            out[t] += y
+            size[t] += np.abs(y)
             # rounding h moves it by 2^-8 of itself; the fp32 sums of g and u move it by their own
             sums = (x.shape[1] / 16 + 16) * 2.0 ** -23
             dh = 2.0 ** -8 * np.abs(h) + sums * (1.1 * b[:H] * np.abs(u) + np.abs(g) * b[H:])
             spread[t] += abs(weights[t, j]) * ((dh + (H / 16 + 16) * 2.0 ** -23 * np.abs(h)) @ np.abs(w_out[e]))
-    return out, hidden, spread
+    return out, hidden, spread, size
 
 
 # ---------------------------------------------------------------- hMLP patchifier (vision)

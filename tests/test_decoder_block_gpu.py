@@ -302,13 +302,13 @@ def check_experts(x, ids, w, w_in, w_out, oracle_mod):
     out = run_experts(x, ids, w, w_in, w_out)
     assert dmel.dmel_last_launch_count() >= 1
     masked = torch.where(ids >= 0, w, torch.zeros_like(w))
-    ref, _, spread = oracle_mod.experts(f64(x), ids.cpu().numpy(), f64(masked), f64(w_in), f64(w_out))
+    ref, _, spread, slots_size = oracle_mod.experts(f64(x), ids.cpu().numpy(), f64(masked), f64(w_in), f64(w_out))
     got = f64(out)
     assert np.isfinite(got).all()
-    # no element beyond what the roundings can do together, and the whole as far off as independent
-    # roundings are: each uniform within half a step, 2^-8 / sqrt 3 of the value at most, for the gated
-    # row and the output
-    sums = ids.shape[1] * 2.0 ** -23 * np.abs(ref)
+    # no element beyond what the roundings can do together (a slot's row to 11 bits among them), and the
+    # whole as far off as independent roundings are: each uniform within half a step, 2^-8 / sqrt 3 of the
+    # value at most, for the gated row and the output (and an eighth of that for the slots' rows)
+    sums = ids.shape[1] * 2.0 ** -23 * np.abs(ref) + 2.0 ** -11 * slots_size
     assert (np.abs(got - ref) <= 2.0 ** -8 * 1.01 * np.abs(ref) + 1.01 * spread + sums + 1e-37).all()
     if ref.size >= 2000:
         assert np.linalg.norm(got - ref) <= 1.25 * 2 ** 0.5 * 2.0 ** -8 / 3 ** 0.5 * np.linalg.norm(ref)
@@ -449,8 +449,8 @@ def test_block_against_the_oracle(n, oracle_mod):
     ids, _ = oracle_mod.route(f64(logits), 2, 3, True, f64(s["bias"]))
     np.testing.assert_array_equal(s["ids"].cpu().numpy(), ids)
     assert (s["ids"][:, 3:] == torch.tensor([16, 17], device=DEV)).all()
-    ref, _, spread = oracle_mod.experts(f64(s["n1"]), ids, f64(s["wts"]), f64(s["w_in"]), f64(s["w_out"]))
-    assert (np.abs(f64(s["moe"]) - ref) <= 2.0 ** -8 * 1.01 * np.abs(ref) + 1.01 * spread + 1e-6 * np.abs(ref)).all()
+    ref, _, spread, size = oracle_mod.experts(f64(s["n1"]), ids, f64(s["wts"]), f64(s["w_in"]), f64(s["w_out"]))
+    assert (np.abs(f64(s["moe"]) - ref) <= 2.0 ** -8 * 1.01 * np.abs(ref) + 1.01 * spread + 2.0 ** -11 * size + 1e-6 * np.abs(ref)).all()
     r2, y2, sc2 = oracle_mod.add_rmsnorm(f64(s["moe"]), f64(mid), f64(s["g2"]), 1e-6, 128)
     assert (np.abs(f64(s["stream"]) - r2) <= 2.0 ** -8 * 1.01 * np.abs(r2)).all()
     each = np.repeat(sc2, 128, axis=1)[:, :264]

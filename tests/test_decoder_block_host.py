@@ -121,9 +121,9 @@ def test_experts_workspace_size(lib):
     size = dmel.dmel_experts_workspace_size
     assert size(0, 6, 32, 6144, 1024) == 0 and size(5, 0, 32, 6144, 1024) == 0 and size(5, 6, 0, 6144, 1024) == 0
     rows = 4096 * 6
-    # the gated rows in bf16, the outputs per slot in fp32, and the plan: rows and tokens of the slots,
+    # the gated rows in bf16, the outputs per slot in 16 bits with a scale per 128 columns, and the plan: rows and tokens of the slots,
     # tiles of at least 32 tokens and one more per expert
-    need = rows * (1024 * 2 + 6144 * 4) + rows * 8 + (rows // 32 + 32) * 16
+    need = rows * (1024 * 2 + 6144 * 2 + 48 * 4) + rows * 8 + (rows // 32 + 32) * 16
     assert need <= size(4096, 6, 32, 6144, 1024) <= need + 6 * 256 + 256
 
 
@@ -207,6 +207,7 @@ def test_oracle_experts_by_hand(oracle_mod):
     w_in[1, 0] = [64.0, 64.0, 2.0, -3.0]
     w_out = np.zeros((2, 2, 3))
     w_out[1] = [[1.0, 0.0, 2.0], [0.0, 1.0, 1.0]]
-    out, h, _ = oracle_mod.experts(x, np.array([[1, -1]]), np.array([[0.5, 9.0]]), w_in, w_out)
+    out, h, _, size = oracle_mod.experts(x, np.array([[1, -1]]), np.array([[0.5, 9.0]]), w_in, w_out)
     np.testing.assert_allclose(h[0, 0], [128.0, -192.0], rtol=1e-14)
     np.testing.assert_allclose(out[0], [64.0, -96.0, 32.0], rtol=1e-14)
+    np.testing.assert_allclose(size[0], [64.0, 96.0, 32.0], rtol=1e-14)
