@@ -53,14 +53,32 @@ struct PlanOut {
   int *row;          // [n_slots] slot -> row, -1 for a slot without an expert
 };
 
-__global__ void __launch_bounds__(kPlanThreads) experts_plan_kernel(const int32_t *__restrict__ ids, int n_slots,
-                                                                    int slots, int E, int tile_tokens, PlanOut out,
+// What a call's kernels share beside the operands of the products.
+struct Shared {
+  const int32_t *ids;
+  const float *weights;
+  int n_slots, slots, n_experts;
+  int splits;           // of the first product's K, joined by the last block of a tile to finish
+  int n_counters;       // per 128 columns of the output: token tiles done; then, with splits, per
+  int *counters;        //   tile and CTA of the first product: splits done
+  float *partial;       // with splits: [tile][split][CTA of the pair][tokens][128]
+  float *scales;        // of the slots' output rows
+  __nv_bfloat16 *out;
+  PlanOut plan;
+};
+
+__global__ void __launch_bounds__(kPlanThreads) experts_plan_kernel(const Shared call, int tile_tokens,
                                                                     uint32_t *err) {
+  const int32_t *const ids = call.ids;
+  const int n_slots = call.n_slots, slots = call.slots, E = call.n_experts;
+  const PlanOut &out = call.plan;
   extern __shared__ int hist[];  // [32 warps][E], the block's totals [E], the experts' first rows [E]
   __shared__ unsigned long long warp_sum[32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int *total = hist + 32 * E, *first = total + E;
   const unsigned block = cluster_ctarank(), blocks = gridDim.x;  // one cluster
+  if (block == 0)
+    for (int i = threadIdx.x; i < call.n_counters; i += kPlanThreads) call.counters[i] = 0;
   launch_dependents();
   // slots per warp, a multiple of 32 (n_slots <= 2^30)
   const int walkers = 32 * (int)blocks, chunk = ((n_slots + walkers - 1) / walkers + 31) / 32 * 32;
@@ -188,17 +206,7 @@ struct SmallPlan {
   int n_tiles;
 };
 
-struct SmallCall {
-  const int32_t *ids;
-  const float *weights;
-  int n_slots, slots, n_experts, n_counters;
-  int *counters;        // per 128 columns of the output: token tiles done
-  float *scales;        // of the slots' output rows
-  __nv_bfloat16 *out;
-  PlanOut plan;
-};
-
-__device__ __forceinline__ void make_small_plan(const SmallCall &c, int tile_tokens, SmallPlan *p, int *expert,
+__device__ __forceinline__ void make_small_plan(const Shared &c, int tile_tokens, SmallPlan *p, int *expert,
                                                 int *starts, bool writer, uint32_t *err) {
   const int n = c.n_slots;
   for (int i = threadIdx.x; i < n; i += blockDim.x) {
@@ -281,6 +289,7 @@ struct EX {
   static constexpr int OFF_STG = OFF_B + STAGES * B_STAGE;
   static constexpr int OFF_BAR = OFF_STG + EPI_GROUPS * STG;
   static constexpr int N_BARS = 2 * STAGES + 4 + 1;
+  static constexpr int OFF_LAST = OFF_BAR + 504;
   static constexpr int OFF_IDX = OFF_BAR + 512;
   static constexpr int OFF_PLAN = OFF_IDX + IDX;
   static constexpr int SMEM_BYTES = OFF_PLAN + PLAN + 1024;
@@ -296,7 +305,7 @@ struct EX {
   static constexpr uint32_t TMEM_COLS = 2 * kTokens < 32 ? 32 : 2 * kTokens;
   static_assert(kTokens % 32 == 0 && kTokens <= 256 && (TMEM_COLS & (TMEM_COLS - 1)) == 0, "token tile");
   static_assert(B_STAGE % 1024 == 0 && STAGES >= 4 && STAGES <= 24, "stages");
-  static_assert(N_BARS * 8 + 8 <= 512 && SMEM_BYTES <= 227 * 1024, "shared memory budget");
+  static_assert(N_BARS * 8 + 8 <= 504 && SMEM_BYTES <= 227 * 1024, "shared memory budget");
 };
 
 // Barrier of 128 threads by number; and one that also ANDs a flag, so that all take the same branch.
@@ -343,9 +352,45 @@ __device__ __forceinline__ float4 row4(const uint2 u, float scale) {
   return make_float4(a.x * scale, a.y * scale, b.x * scale, b.y * scale);
 }
 
+// Called by the 256 epilogue threads after their writes of a work item: whether this is the last of n
+// items to come here (whatever the order), whose threads then see the others' writes. Nothing waits.
+__device__ __forceinline__ bool last_of(int n, int *counter, int *flag) {
+  __threadfence();
+  asm volatile("bar.sync 3, 256;" ::: "memory");
+  if (threadIdx.x == 64) {
+    __threadfence();
+    *flag = atomicAdd(counter, 1) == n - 1;
+    __threadfence();
+  }
+  asm volatile("bar.sync 3, 256;" ::: "memory");
+  return *flag != 0;
+}
+
+// The gated rows of a tile whose K was split: the splits' partial sums in order.
+template <int kTokens>
+__device__ __forceinline__ void join_splits(const Shared &c, __nv_bfloat16 *h, int64_t tile, int rank, const TokenTile &tt,
+                                            int hidden, int col) {
+  const int et = threadIdx.x - 64, q = 4 * (et & 15);
+  if (col + q >= hidden) return;
+  const float *base = c.partial + (tile * c.splits * 2 + rank) * kTokens * 128 + q;
+  for (int k = et >> 4; k < tt.rows; k += 16) {
+    float4 g = make_float4(0.0f, 0.0f, 0.0f, 0.0f), u = g;
+#pragma unroll 4
+    for (int s = 0; s < c.splits; ++s) {
+      const float *p = base + ((int64_t)s * 2 * kTokens + k) * 128;
+      const float4 a = __ldcg(reinterpret_cast<const float4 *>(p)), b = __ldcg(reinterpret_cast<const float4 *>(p + 64));
+      g.x += a.x; g.y += a.y; g.z += a.z; g.w += a.w;
+      u.x += b.x; u.y += b.y; u.z += b.z; u.w += b.w;
+    }
+    const float4 y = silu_times(g, u);
+    *reinterpret_cast<uint2 *>(h + (int64_t)(tt.row0 + k) * hidden + col + q) =
+        make_uint2(pack_bf16(y.x, y.y), pack_bf16(y.z, y.w));
+  }
+}
+
 // 128 columns from `col` on of every token's weighted sum, by the 256 epilogue threads: the rows y
 // (dim columns each, other blocks' work among them) in slot order.
-__device__ __forceinline__ void small_sum(const SmallCall &c, const float *y, int dim, int col) {
+__device__ __forceinline__ void small_sum(const Shared &c, const float *y, int dim, int col) {
   const int et = threadIdx.x - 64, q = col + 4 * (et & 31), n_tokens = c.n_slots / c.slots;
   if (q >= dim) return;
   for (int t = et >> 5; t < n_tokens; t += 8) {
@@ -366,12 +411,13 @@ __device__ __forceinline__ void small_sum(const SmallCall &c, const float *y, in
   }
 }
 
-// kSmall: the gate's kernel makes the plan, the down product's kernel the tokens' sums (SmallCall).
-template <int kTokens, bool kGate, bool kSmall>
+// kSmall: the gate's kernel makes the plan, the down product's kernel the tokens' sums (Shared).
+// kSplit: K in parts (of the gate's kernel).
+template <int kTokens, bool kGate, bool kSmall, bool kSplit>
 __global__ void __launch_bounds__(kGate ? EX<kTokens, kSmall>::THREADS_GATE : EX<kTokens, kSmall>::THREADS, 1)
     experts_product_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
                            const __grid_constant__ CUtensorMap xmap8, const int *__restrict__ n_tiles,
-                           const TokenTile *tiles, const int *token, int K, int cols, void *out, const SmallCall small,
+                           const TokenTile *tiles, const int *token, int K, int cols, void *out, const Shared shared,
                            uint32_t *err) {
   using X = EX<kTokens, kSmall>;
   constexpr int STAGES = X::STAGES, BK = X::BK;
@@ -420,7 +466,7 @@ __global__ void __launch_bounds__(kGate ? EX<kTokens, kSmall>::THREADS_GATE : EX
   if (kSmall && kGate) {
     SmallPlan *p = reinterpret_cast<SmallPlan *>(smem + X::OFF_PLAN);
     int *scratch = reinterpret_cast<int *>(smem + X::OFF_STG);  // (the epilogue's, not yet in use)
-    make_small_plan(small, kTokens, p, scratch, scratch + kSmallSlots, blockIdx.x == 0, err);
+    make_small_plan(shared, kTokens, p, scratch, scratch + kSmallSlots, blockIdx.x == 0, err);
     token_tiles = p->n_tiles;
     tiles = p->tiles;
     token = p->token;
@@ -429,11 +475,17 @@ __global__ void __launch_bounds__(kGate ? EX<kTokens, kSmall>::THREADS_GATE : EX
   }
 
   const int n_ct = (cols + 2 * COLS - 1) / (2 * COLS);  // column tiles
-  const int64_t total = (int64_t)token_tiles * n_ct;
+  const int splits = kSplit ? shared.splits : 1;
+  const int64_t total = (int64_t)token_tiles * n_ct * splits;
   const int KB = (K + BK - 1) / BK;
   const int64_t step = gridDim.x >> 1;
-  // consecutive pairs take the column tiles of one token tile (its rows stay in L2)
-  auto tile_at = [&](int64_t t) { return tiles[t / n_ct]; };
+  // Work item u: split u % splits of K (blocks kb0 .. kb1 - 1) of tile u / splits. Consecutive pairs
+  // take the column tiles of one token tile (its rows stay in L2).
+  auto tile_of = [&](int64_t u) { return kSplit ? u / splits : u; };
+  auto token_tile = [&](int64_t u) { return tiles[tile_of(u) / n_ct]; };
+  auto column = [&](int64_t u) { return (int)(tile_of(u) % n_ct) * 2 * COLS + (int)rank * COLS; };
+  auto kb_begin = [&](int64_t u) { return kSplit ? KB * (int)(u % splits) / splits : 0; };
+  auto kb_end = [&](int64_t u) { return kSplit ? KB * ((int)(u % splits) + 1) / splits : KB; };
 
   if (warp == 0) {
     // ------------------------------------------------ TMA: weight boxes, and consecutive rows
@@ -441,11 +493,11 @@ __global__ void __launch_bounds__(kGate ? EX<kTokens, kSmall>::THREADS_GATE : EX
     uint32_t phase = 0, pending = 0, pending_phase = 0;
     bool ok = true;
     for (int64_t t = blockIdx.x >> 1; ok && t < total; t += step) {
-      const TokenTile tt = tile_at(t);
-      const int col = (int)(t % n_ct) * 2 * COLS + (int)rank * COLS;
+      const TokenTile tt = token_tile(t);
+      const int col = column(t), kb1 = kb_end(t);
       const int half = tt.width / 2;  // token rows of this CTA, a multiple of 8
       const uint32_t bytes = 2u * (X::A_STAGE + (uint32_t)half * 128u);
-      for (int kb = 0; kb < KB; ++kb) {
+      for (int kb = kb_begin(t); kb < kb1; ++kb) {
         if (!__all_sync(kAll, mbar_wait(empty(stage), phase ^ 1u, err))) { ok = false; break; }
         if (elect_one()) {
           if (leader) mbar_arrive_expect_tx(full(stage), bytes);
@@ -481,11 +533,12 @@ __global__ void __launch_bounds__(kGate ? EX<kTokens, kSmall>::THREADS_GATE : EX
       bool ok = true;
       for (int64_t t = blockIdx.x >> 1; ok && t < total; t += step, ++i) {
         const uint32_t acc = i & 1u, use = i >> 1;
-        const uint32_t idesc = idesc_bf16_f32(256, (uint32_t)tile_at(t).width, 0, 1);
+        const uint32_t idesc = idesc_bf16_f32(256, (uint32_t)token_tile(t).width, 0, 1);
+        const int kb0 = kb_begin(t), kb1 = kb_end(t);
         if (!__all_sync(kAll, mbar_wait(tempty(acc), (use & 1u) ^ 1u, err))) break;
         tc_fence_after();
         const uint32_t d = tmem_base + acc * X::ACC_STRIDE;
-        for (int kb = 0; kb < KB; ++kb) {
+        for (int kb = kb0; kb < kb1; ++kb) {
           if (!__all_sync(kAll, mbar_wait(full(stage), phase, err))) { ok = false; break; }
           tc_fence_after();
           const uint32_t a0 = smem_addr(smem + stage * X::A_STAGE);
@@ -497,7 +550,7 @@ __global__ void __launch_bounds__(kGate ? EX<kTokens, kSmall>::THREADS_GATE : EX
               const uint64_t adesc = smem_desc(a0 + 2048u * k, (uint32_t)X::BOX, 1024u, kSwizzle128B);
               // tokens: K-major, 8-row groups 1024 B apart, 32 B per step
               const uint64_t bdesc = smem_desc(b0 + 32u * k, 16u, 1024u, kSwizzle128B);
-              tc_mma_f16_pair(d, adesc, bdesc, idesc, (kb | k) != 0 ? 1u : 0u);
+              tc_mma_f16_pair(d, adesc, bdesc, idesc, kb > kb0 || k > 0 ? 1u : 0u);
             }
             tc_commit_pair_both(empty(stage), 3);
           }
@@ -521,8 +574,8 @@ __global__ void __launch_bounds__(kGate ? EX<kTokens, kSmall>::THREADS_GATE : EX
     uint32_t phase = 0;
     bool ok = true;
     for (int64_t t = blockIdx.x >> 1; ok && t < total; t += step) {
-      const TokenTile tt = tile_at(t);
-      const int groups = tt.width / 8;  // of four rows, in this CTA's half
+      const TokenTile tt = token_tile(t);
+      const int kb1 = kb_end(t), groups = tt.width / 8;  // of four rows, in this CTA's half
       __syncwarp();                     // the last tile's numbers have been read
       for (int g = w + X::GATHER_WARPS * lane; g < groups; g += X::GATHER_WARPS * 32) {
         int r[4];
@@ -534,7 +587,7 @@ __global__ void __launch_bounds__(kGate ? EX<kTokens, kSmall>::THREADS_GATE : EX
         idx[g] = make_int4(r[0], r[1], r[2], r[3]);
       }
       __syncwarp();
-      for (int kb = 0; kb < KB; ++kb) {
+      for (int kb = kb_begin(t); kb < kb1; ++kb) {
         if (!__all_sync(kAll, mbar_wait(empty(stage), phase ^ 1u, err))) { ok = false; break; }
         if (elect_one()) {
           const uint32_t fb = mapa_shared(full(stage), 0);
@@ -555,12 +608,13 @@ __global__ void __launch_bounds__(kGate ? EX<kTokens, kSmall>::THREADS_GATE : EX
     // each through a staging buffer of its own.
     const int quad = warp & 3, group = (warp - 2) >> 2, et = (threadIdx.x - 64) & 127;
     float *const buf = reinterpret_cast<float *>(smem + X::OFF_STG + group * X::STG);
+    int *last = reinterpret_cast<int *>(smem + X::OFF_LAST);
     uint32_t i = 0;
     bool ok = true;
     for (int64_t t = blockIdx.x >> 1; t < total; t += step, ++i) {
       const uint32_t acc = i & 1u, use = i >> 1;
-      const TokenTile tt = tile_at(t);
-      const int col = (int)(t % n_ct) * 2 * COLS + (int)rank * COLS;
+      const TokenTile tt = token_tile(t);
+      const int col = column(t);
       ok = group_bar_and(1 + group, ok && mbar_wait(tfull(acc), use & 1u, err));
       tc_fence_after();
       const uint32_t tb = tmem_base + ((uint32_t)(32 * quad) << 16) + acc * X::ACC_STRIDE;
@@ -580,7 +634,15 @@ __global__ void __launch_bounds__(kGate ? EX<kTokens, kSmall>::THREADS_GATE : EX
         }
         group_bar(1 + group);
         const int n_tok = tt.rows - c < 32 ? tt.rows - c : 32;
-        if (kGate) {
+        if (kSplit) {
+          float *part = shared.partial + ((t * 2 + rank) * kTokens + c) * 128 + 4 * (et & 31);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const int k = (et >> 5) + 4 * j;
+            const float4 r = *reinterpret_cast<const float4 *>(buf + k * 128 + 4 * (et & 31));
+            if (k < n_tok) *reinterpret_cast<float4 *>(part + k * 128) = r;
+          }
+        } else if (kGate) {
           __nv_bfloat16 *h = static_cast<__nv_bfloat16 *>(out) + (int64_t)(tt.row0 + c) * cols + col;
           const int q = et & 15, k0 = et >> 4;  // 4 columns, a token per 16 threads
           if (col + 4 * q < cols) {
@@ -610,7 +672,7 @@ __global__ void __launch_bounds__(kGate ? EX<kTokens, kSmall>::THREADS_GATE : EX
           } else {
             __half *y = static_cast<__half *>(out) + row0 * cols + col + 4 * q;
             const int n_blocks = (cols + 127) / 128;
-            float *scales = small.scales + row0 * n_blocks + col / 128;
+            float *scales = shared.scales + row0 * n_blocks + col / 128;
             float up[8];
             // (columns past the last are zeros: the weights' fill)
 #pragma unroll
@@ -636,23 +698,19 @@ __global__ void __launch_bounds__(kGate ? EX<kTokens, kSmall>::THREADS_GATE : EX
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_remote(mapa_shared(tempty(acc), 0));
+      if (kSplit) {
+        if (last_of(splits, shared.counters + 2 * ((K + 255) / 256) + 2 * tile_of(t) + rank, last))
+          join_splits<kTokens>(shared, static_cast<__nv_bfloat16 *>(out), tile_of(t), (int)rank, tt, cols, col);
+      }
       if (kSmall && !kGate) {
-        // the last block to finish these columns (in whatever order) sums them for every token
-        int *last = reinterpret_cast<int *>(smem + X::OFF_IDX);
-        __threadfence();
-        asm volatile("bar.sync 3, %0;" ::"n"(32 * X::EPI_WARPS) : "memory");
-        if (threadIdx.x == 64) {
-          __threadfence();
-          *last = atomicAdd(small.counters + 2 * (t % n_ct) + rank, 1) == token_tiles - 1;
-          __threadfence();
-        }
-        asm volatile("bar.sync 3, %0;" ::"n"(32 * X::EPI_WARPS) : "memory");
-        if (*last) small_sum(small, static_cast<const float *>(out), cols, col);
+        // these columns of all tokens, when every token tile has been through them
+        if (last_of(token_tiles, shared.counters + 2 * (t % n_ct) + rank, last))
+          small_sum(shared, static_cast<const float *>(out), cols, col);
       }
     }
     if (kSmall && !kGate && token_tiles == 0)  // no token has an expert: zeros
       for (int64_t ct = blockIdx.x >> 1; ct < n_ct; ct += step)
-        small_sum(small, static_cast<const float *>(out), cols, (int)ct * 2 * COLS + (int)rank * COLS);
+        small_sum(shared, static_cast<const float *>(out), cols, (int)ct * 2 * COLS + (int)rank * COLS);
   }
 
   tc_fence_before();
@@ -699,16 +757,44 @@ __global__ void __launch_bounds__(256) experts_sum_kernel(const __half *__restri
 
 size_t r256(size_t x) { return (x + 255) / 256 * 256; }
 
-constexpr int kMinTile = 32;  // the narrowest token tile of the product kernels
+constexpr int kPairs = 74;  // pairs of a B200's 148 SMs, for rules that a workspace's size depends on
+
+// How a call is run, from its sizes alone.
+struct Config {
+  bool small;         // plan and sums inside the products
+  int tile_tokens;    // the products' token tiles
+  int splits;         // of the first product's K
+  int64_t max_tiles;  // token tiles at most
+  int n_counters;
+};
+
+Config config(int64_t n_tokens, int slots, const dmel_expert_weights &w) {
+  Config c;
+  const int64_t n = n_tokens * slots;
+  // Tiles of 32 tokens (ten stages of weights in flight) where an expert has few on average: the
+  // weights' bytes and latency bound such calls (128 slots on 8 experts, 2048 / 512: 29 us, 33 with
+  // tiles of 128, 35 with 256). Wider ones share a pass over the weights between their tokens (1,536
+  // slots on 32 experts, 6144 / 1024: 335, 218 and 221 us; 6,144 slots: 1,014, 406 and 319 us).
+  c.tile_tokens = n <= kSmallSlots || n <= 16 * (int64_t)w.n_experts ? 32 : n <= 64 * (int64_t)w.n_experts ? 128 : 256;
+  c.max_tiles = n / c.tile_tokens + (n < w.n_experts ? n : w.n_experts);
+  // The first product's K in up to 8 parts of 16 blocks or more where its tiles would leave half of
+  // the pairs of CTAs without work
+  const int64_t tiles = c.max_tiles * ((w.hidden + 127) / 128);
+  int64_t splits = kPairs / tiles, most = (w.dim + 63) / 64 / 16;
+  if (splits > 8) splits = 8;
+  if (splits > most) splits = most;
+  c.splits = splits > 1 ? (int)splits : 1;
+  c.small = n <= kSmallSlots;
+  c.n_counters = (w.dim + 255) / 256 * 2 + (c.splits > 1 ? 2 * (int)tiles : 0);
+  return c;
+}
 
 struct Layout {
-  size_t n_tiles, counters, tiles, token, row, h, y, scales, total;
+  size_t n_tiles, counters, tiles, token, row, h, y, scales, partial, total;
 };
 Layout layout(int64_t n_tokens, int slots, const dmel_expert_weights &w) {
+  const Config c = config(n_tokens, slots, w);
   const size_t n = (size_t)n_tokens * slots;
-  // one tile per started kMinTile tokens of an expert
-  const size_t tiles = n / kMinTile + (n < (size_t)w.n_experts ? n : (size_t)w.n_experts);
-  // (counters: one per 128 columns of the output, in pairs)
   Layout L;
   size_t at = 0;
   auto take = [&](size_t bytes) {
@@ -717,13 +803,14 @@ Layout layout(int64_t n_tokens, int slots, const dmel_expert_weights &w) {
     return here;
   };
   L.n_tiles = take(4);
-  L.counters = take((size_t)(w.dim + 255) / 256 * 2 * 4);
-  L.tiles = take(tiles * sizeof(TokenTile));
+  L.counters = take((size_t)c.n_counters * 4);
+  L.tiles = take((size_t)c.max_tiles * sizeof(TokenTile));
   L.token = take(n * 4);
   L.row = take(n * 4);
   L.h = take(n * w.hidden * 2);
-  L.y = take(n * w.dim * (n <= (size_t)kSmallSlots ? 4 : 2));
+  L.y = take(n * w.dim * (c.small ? 4 : 2));
   L.scales = take(n * ((w.dim + 127) / 128) * 4);
+  L.partial = take(c.splits > 1 ? (size_t)c.max_tiles * ((w.hidden + 127) / 128) * c.splits * 2 * c.tile_tokens * 128 * 4 : 0);
   L.total = at;
   return L;
 }
@@ -755,22 +842,23 @@ struct Call {
   CUtensorMap in_w, in_x, out_w, out_h, out_h8;
   int dim, hidden;
   void *h, *y;
-  SmallCall small;
+  Shared shared;
   int64_t max_tiles;
   uint32_t *err;
   int num_sms;
   cudaStream_t stream;
 };
 
-template <int kTokens, bool kGate, bool kSmall>
+template <int kTokens, bool kGate, bool kSmall, bool kSplit>
 cudaError_t launch_product(const Call &c) {
   using X = EX<kTokens, kSmall>;
   static std::atomic<bool> attr[256];
-  const auto kernel = experts_product_kernel<kTokens, kGate, kSmall>;
+  const auto kernel = experts_product_kernel<kTokens, kGate, kSmall, kSplit>;
   const cudaError_t e = set_smem_attr_once(kernel, X::SMEM_BYTES, attr);
   if (e != cudaSuccess) return e;
   const int cols = kGate ? c.hidden : c.dim, per_pair = kGate ? 128 : 256;
-  const int64_t work = c.max_tiles * ((cols + per_pair - 1) / per_pair), pairs = c.num_sms / 2 > 0 ? c.num_sms / 2 : 1;
+  const int64_t work = c.max_tiles * ((cols + per_pair - 1) / per_pair) * (kGate ? c.shared.splits : 1);
+  const int64_t pairs = c.num_sms / 2 > 0 ? c.num_sms / 2 : 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(2 * (work < pairs ? work : pairs)));
   cfg.blockDim = dim3(kGate ? X::THREADS_GATE : X::THREADS);
@@ -785,18 +873,22 @@ cudaError_t launch_product(const Call &c) {
   at[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = kSmall && kGate ? 1 : 2;  // (the first launch of a call starts when all before it is done)
-  const PlanOut &p = c.small.plan;
+  const PlanOut &p = c.shared.plan;
   return cudaLaunchKernelEx(&cfg, kernel, kGate ? c.in_w : c.out_w, kGate ? c.in_x : c.out_h, c.out_h8,
                             (const int *)p.n_tiles, (const TokenTile *)p.tiles, (const int *)p.token,
-                            kGate ? c.dim : c.hidden, cols, kGate ? c.h : c.y, c.small, c.err);
+                            kGate ? c.dim : c.hidden, cols, kGate ? c.h : c.y, c.shared, c.err);
 }
 
-template <int kTokens, bool kSmall>
+template <int kTokens, bool kSmallGate, bool kSmallDown>
 cudaError_t launch_products(const Call &c, int *launches) {
-  cudaError_t e = launch_product<kTokens, true, kSmall>(c);
+  cudaError_t e;
+  if constexpr (!kSmallGate)
+    e = c.shared.splits > 1 ? launch_product<kTokens, true, false, true>(c) : launch_product<kTokens, true, false, false>(c);
+  else
+    e = launch_product<kTokens, true, true, false>(c);
   if (e != cudaSuccess) return e;
   ++*launches;
-  e = launch_product<kTokens, false, kSmall>(c);
+  e = launch_product<kTokens, false, kSmallDown, false>(c);
   if (e == cudaSuccess) ++*launches;
   return e;
 }
@@ -805,7 +897,7 @@ cudaError_t launch_plan(const Call &c, int tile_tokens, int *launches) {
   static std::atomic<bool> attr[256];
   cudaError_t e = set_smem_attr_once(experts_plan_kernel, 34 * 1024 * 4, attr);
   if (e != cudaSuccess) return e;
-  const SmallCall &s = c.small;
+  const Shared &s = c.shared;
   const unsigned blocks = s.n_slots > 1024 ? 8 : 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(blocks);
@@ -819,7 +911,7 @@ cudaError_t launch_plan(const Call &c, int tile_tokens, int *launches) {
   at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, experts_plan_kernel, s.ids, s.n_slots, s.slots, s.n_experts, tile_tokens, s.plan, c.err);
+  e = cudaLaunchKernelEx(&cfg, experts_plan_kernel, s, tile_tokens, c.err);
   if (e == cudaSuccess) ++*launches;
   return e;
 }
@@ -835,8 +927,8 @@ cudaError_t launch_sum(const Call &c, int64_t n_tokens, int *launches) {
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, experts_sum_kernel, (const __half *)c.y, (const float *)c.small.scales, (const int *)c.small.plan.row,
-                                           c.small.weights, n_tokens, c.small.slots, c.dim, c.small.out);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, experts_sum_kernel, (const __half *)c.y, (const float *)c.shared.scales, (const int *)c.shared.plan.row,
+                                           c.shared.weights, n_tokens, c.shared.slots, c.dim, c.shared.out);
   if (e == cudaSuccess) ++*launches;
   return e;
 }
@@ -852,6 +944,7 @@ cudaError_t launch_experts(const void *x, int64_t n_tokens, const int32_t *ids, 
                            cudaStream_t stream, int *launches) {
   EncodeTiledFn enc = encode_tiled_fn();
   if (!enc) return cudaErrorNotSupported;
+  const Config cf = config(n_tokens, slots, w);
   const Layout L = layout(n_tokens, slots, w);
   uint8_t *base = static_cast<uint8_t *>(workspace);
   const int n_slots = (int)(n_tokens * slots);
@@ -863,13 +956,15 @@ cudaError_t launch_experts(const void *x, int64_t n_tokens, const int32_t *ids, 
   c.err = err;
   c.num_sms = num_sms;
   c.stream = stream;
-  SmallCall &s = c.small;
+  Shared &s = c.shared;
   s.ids = ids;
   s.weights = weights;
   s.n_slots = n_slots;
   s.slots = slots;
   s.n_experts = w.n_experts;
-  s.n_counters = (w.dim + 255) / 256 * 2;
+  s.splits = cf.splits;
+  s.n_counters = cf.n_counters;
+  s.partial = reinterpret_cast<float *>(base + L.partial);
   s.counters = reinterpret_cast<int *>(base + L.counters);
   s.scales = reinterpret_cast<float *>(base + L.scales);
   s.out = static_cast<__nv_bfloat16 *>(out);
@@ -881,14 +976,15 @@ cudaError_t launch_experts(const void *x, int64_t n_tokens, const int32_t *ids, 
       !row_map(&c.in_x, enc, x, n_tokens, w.dim, 1) || !weight_map(&c.out_w, enc, w.w_out, w.n_experts, w.hidden, w.dim) ||
       !row_map(&c.out_h, enc, c.h, n_slots, w.hidden, 32) || !row_map(&c.out_h8, enc, c.h, n_slots, w.hidden, 8))
     return cudaErrorInvalidValue;
-  // Tiles of 32 tokens (ten stages of weights in flight) where an expert has 16 or fewer on average:
-  // the weights' bytes bound such calls; else wide ones, whose tokens share a pass over the weights.
-  const bool small = n_slots <= kSmallSlots, narrow = small || n_slots <= 16 * (int64_t)w.n_experts;
-  const int tile_tokens = narrow ? 32 : 256;
-  c.max_tiles = n_slots / tile_tokens + (n_slots < w.n_experts ? n_slots : w.n_experts);
-  if (small) return launch_products<32, true>(c, launches);
-  cudaError_t e = launch_plan(c, tile_tokens, launches);
-  if (e == cudaSuccess) e = narrow ? launch_products<32, false>(c, launches) : launch_products<256, false>(c, launches);
+  c.max_tiles = cf.max_tiles;
+  cudaError_t e = cudaSuccess;
+  // the splits' counters are cleared by the plan's kernel
+  if (cf.small && cf.splits == 1) return launch_products<32, true, true>(c, launches);
+  if ((e = launch_plan(c, cf.tile_tokens, launches)) != cudaSuccess) return e;
+  if (cf.small) return launch_products<32, false, true>(c, launches);
+  e = cf.tile_tokens == 32    ? launch_products<32, false, false>(c, launches)
+      : cf.tile_tokens == 128 ? launch_products<128, false, false>(c, launches)
+                              : launch_products<256, false, false>(c, launches);
   return e == cudaSuccess ? launch_sum(c, n_tokens, launches) : e;
 }
 

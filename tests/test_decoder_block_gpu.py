@@ -320,7 +320,9 @@ def check_experts(x, ids, w, w_in, w_out, oracle_mod):
     (1, 1, 1, 8, 8), (1, 6, 32, 512, 128), (2, 3, 4, 72, 40), (5, 2, 3, 200, 264), (40, 2, 2, 136, 72),
     (300, 2, 3, 264, 136), (257, 1, 1, 64, 64), (700, 3, 7, 328, 200), (64, 8, 96, 128, 64), (33, 64, 5, 64, 24),
     (1100, 4, 2, 64, 520), (3, 2, 1024, 24, 16), (171, 3, 40, 72, 40), (64, 1, 1, 64, 264), (65, 1, 1, 64, 72),
-    (16, 4, 33, 520, 136), (32, 2, 3, 264, 72), (13, 5, 9, 520, 136)])
+    (16, 4, 33, 520, 136), (32, 2, 3, 264, 72), (13, 5, 9, 520, 136),
+    # the first product's K in parts: 2, 4, 4, 2, 3
+    (5, 2, 3, 2056, 72), (40, 2, 2, 4104, 136), (1, 1, 2, 4096, 64), (700, 1, 1, 2200, 200), (130, 3, 5, 3080, 264)])
 def test_experts(n, slots, e, d, h, oracle_mod):
     check_experts(*expert_inputs(n + d, n, slots, e, d, h), oracle_mod)
 

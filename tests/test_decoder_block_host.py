@@ -122,8 +122,8 @@ def test_experts_workspace_size(lib):
     assert size(0, 6, 32, 6144, 1024) == 0 and size(5, 0, 32, 6144, 1024) == 0 and size(5, 6, 0, 6144, 1024) == 0
     rows = 4096 * 6
     # the gated rows in bf16, the outputs per slot in 16 bits with a scale per 128 columns, and the plan: rows and tokens of the slots,
-    # tiles of at least 32 tokens and one more per expert
-    need = rows * (1024 * 2 + 6144 * 2 + 48 * 4) + rows * 8 + (rows // 32 + 32) * 16
+    # tiles of 256 tokens and one more per expert
+    need = rows * (1024 * 2 + 6144 * 2 + 48 * 4) + rows * 8 + (rows // 256 + 32) * 16
     assert need <= size(4096, 6, 32, 6144, 1024) <= need + 6 * 256 + 256
 
 
