@@ -62,17 +62,17 @@ __device__ __forceinline__ float value_of(float k) {  // cut towards -inf, by le
   return __uint_as_float(u >> 31 ? u | (N - 1) : u & ~(uint32_t)(N - 1));
 }
 
-// Bounds on the fp32 scores' errors: a sigmoid's 6e-7 (exp and reciprocal of a few ulps), a
-// softmax's 2e-6 (the same, and a sum of up to 1,056 terms by pairs).
-constexpr float kSigmoidOff = 6e-7f, kSoftmaxOff = 2e-6f;
+// Bounds on the fp32 scores' errors, from ex2.approx's 2^-22 and rcp.approx's 2^-23 of the result and
+// the roundings around them. A sigmoid's: 3e-7 (the exponential's error counts s (1 - s) at most). A
+// softmax's, with its sum of up to 1,056 terms by pairs: 1.8e-6 of the token's largest score, 1 / z.
+constexpr float kSigmoidOff = 3.5e-7f, kSoftmaxOff = 2e-6f;
 
 // How far apart two choice values must be for their keys, a above b, to order them as 64-bit
-// arithmetic does: twice the score's error, the rounding of the sums with the bias, and what
-// key_of<N> may have cut off b. Logits (not scored) are off only by what is cut.
+// arithmetic does: twice the score's error `off` (0 for logits), the rounding of the sums with the
+// bias, and what key_of<N> may have cut off b.
 template <int N>
-__device__ __forceinline__ float margin(bool scored, bool sigmoid, float a, float b) {
-  const float off = scored ? 2.0f * (sigmoid ? kSigmoidOff : kSoftmaxOff) : 0.0f;
-  return off + (N + 2) * 1.2e-7f * fmaxf(fabsf(a), fabsf(b));
+__device__ __forceinline__ float margin(float off, float a, float b) {
+  return 2.0f * off + (N + 2) * 1.2e-7f * fmaxf(fabsf(a), fabsf(b));
 }
 
 // exp and 1 / x on the special-function unit (a few ulps, results below the normal range zero).
@@ -261,7 +261,7 @@ __device__ __noinline__ int choose_fp64(const T *row, const float *bias, const S
 
 // kScored: the choice compares scores (a bias, or groups), else the logits themselves.
 template <typename T, int EPL, bool kScored, bool kGroups>
-__global__ void __launch_bounds__(32 * kWarps) route_kernel(const T *__restrict__ logits, int64_t n_tokens,
+__global__ void __launch_bounds__(32 * kWarps, 7) route_kernel(const T *__restrict__ logits, int64_t n_tokens,
                                                             const float *__restrict__ bias, const Settings q,
                                                             int32_t *__restrict__ ids, float *__restrict__ weights) {
   const dmel_router &r = q.r;
@@ -297,8 +297,10 @@ __global__ void __launch_bounds__(32 * kWarps) route_kernel(const T *__restrict_
     // what the choice compares, -inf for what is not to be chosen
     bool unsure = false;
     float v[EPL];
+    float off = 0.0f;  // the scores' error
     if (kScored) {
       const float inv_z = fast_rcp(z);
+      off = sigmoid ? kSigmoidOff : kSoftmaxOff * inv_z;
 #pragma unroll
       for (int i = 0; i < EPL; ++i) {
         const float s = sigmoid ? fast_rcp(1.0f + fast_exp(-l[i])) : fast_exp(l[i] - top) * inv_z;
@@ -324,8 +326,7 @@ __global__ void __launch_bounds__(32 * kWarps) route_kernel(const T *__restrict_
       __syncwarp();
       float worst, best;
       const unsigned kept = keep_groups(narrow, q, &worst, &best);
-      // two scores per rating, of which a softmax's are at most 1 together
-      unsure = best > kNone && !(worst - best > (sigmoid ? 2.0f : 1.0f) * margin<1>(true, sigmoid, worst, best));
+      unsure = best > kNone && !(worst - best > margin<1>(2.0f * off, worst, best));  // (two scores a rating)
 #pragma unroll
       for (int i = 0; i < EPL; ++i) {
         const float x = bias ? v[i] : l[i];
@@ -348,7 +349,7 @@ __global__ void __launch_bounds__(32 * kWarps) route_kernel(const T *__restrict_
       const float b = value_of<EPL>(best);
       if (lane == k) my_id = idx;
       // nearer than they may be off; two experts alike are a tie, which goes by index here as well
-      if (k > 0 && !(last_v - b > margin<EPL>(bias != nullptr, sigmoid, last_v, b)) &&
+      if (k > 0 && !(last_v - b > margin<EPL>(bias ? off : 0.0f, last_v, b)) &&
           !(at(last) == at(idx) && (!bias || __ldg(bias + last) == __ldg(bias + idx))))
         unsure = true;
       last = idx;
