@@ -95,17 +95,21 @@ __global__ void __launch_bounds__(kPlanThreads) experts_plan_kernel(const Shared
     const int e = ids[i];
     return e >= 0 && e < E ? e : -1;
   };
-  for (int i = begin; i < end; i += 32 * kAhead) {
-    int e[kAhead];
+  int e[kAhead], rank[kAhead];  // of a batch's slots: the expert, and the warp's slots of it before
+  auto count_batch = [&](int i) {
 #pragma unroll
     for (int a = 0; a < kAhead; ++a) e[a] = expert_at(i + 32 * a + lane);
 #pragma unroll
     for (int a = 0; a < kAhead; ++a) {
+      if (i + 32 * a >= end) break;
       const unsigned peers = __match_any_sync(kAll, e[a]);
+      rank[a] = e[a] >= 0 ? hist[warp * E + e[a]] + __popc(peers & ((1u << lane) - 1u)) : 0;
+      __syncwarp();
       if (e[a] >= 0 && lane == __ffs(peers) - 1) hist[warp * E + e[a]] += __popc(peers);
       __syncwarp();
     }
-  }
+  };
+  for (int i = begin; i < end; i += 32 * kAhead) count_batch(i);
   __syncthreads();
   // counts -> exclusive row offsets within the expert, per warp of this block; then over the blocks
   int count = 0, tiles = 0, before_block = 0;
@@ -171,24 +175,22 @@ __global__ void __launch_bounds__(kPlanThreads) experts_plan_kernel(const Shared
   }
   if (threadIdx.x == kPlanThreads - 1 && block == 0) *out.n_tiles = (int)((before + own) >> 32);
   __syncthreads();
+  // hist now has the rows before the warp's own. The last batch's ranks are still there: with one
+  // batch per warp (65,536 slots) no slot is matched twice.
   for (int i = begin; i < end; i += 32 * kAhead) {
-    int e[kAhead];
-#pragma unroll
-    for (int a = 0; a < kAhead; ++a) e[a] = expert_at(i + 32 * a + lane);
+    if (chunk > 32 * kAhead) count_batch(i);  // (on from the offset, so these ranks include it)
 #pragma unroll
     for (int a = 0; a < kAhead; ++a) {
-      const unsigned peers = __match_any_sync(kAll, e[a]);
-      int pos = -1;
-      if (e[a] >= 0) pos = first[e[a]] + hist[warp * E + e[a]] + __popc(peers & ((1u << lane) - 1u));
-      __syncwarp();
-      if (e[a] >= 0 && lane == __ffs(peers) - 1) hist[warp * E + e[a]] += __popc(peers);
-      __syncwarp();
       const int slot = i + 32 * a + lane;
-      if (slot < end) {
-        out.row[slot] = pos;
-        if (pos >= 0) out.token[pos] = slot / slots;
-        else if (ids[slot] != -1) record_error(err, DMEL_DEVERR_EXPERT);
+      if (slot >= end) break;
+      int pos = -1;
+      if (e[a] >= 0) {
+        pos = first[e[a]] + rank[a] + (chunk > 32 * kAhead ? 0 : hist[warp * E + e[a]]);
+        out.token[pos] = slot / slots;
+      } else if (ids[slot] != -1) {
+        record_error(err, DMEL_DEVERR_EXPERT);
       }
+      out.row[slot] = pos;
     }
   }
 }

@@ -327,6 +327,22 @@ def test_experts(n, slots, e, d, h, oracle_mod):
     check_experts(*expert_inputs(n + d, n, slots, e, d, h), oracle_mod)
 
 
+@pytest.mark.parametrize("n,slots,e,d,h", [(30000, 5, 3, 16, 8), (20000, 6, 32, 16, 8), (1500, 1, 1000, 16, 8)])
+def test_experts_many_slots(n, slots, e, d, h):
+    """Plans of several blocks and batches: against the formula in fp64, expert by expert."""
+    x, ids, w, w_in, w_out = expert_inputs(n, n, slots, e, d, h, empty=0.1)
+    out = run_experts(x, ids, w, w_in, w_out)
+    ref = torch.zeros((n, d), dtype=torch.float64, device=DEV)
+    for i in range(e):
+        t, j = torch.nonzero(ids == i, as_tuple=True)
+        a = x[t].double() @ w_in[i].double()
+        y = torch.nn.functional.silu(a[:, :h]) * a[:, h:] @ w_out[i].double()
+        ref.index_add_(0, t, y * w[t, j].double()[:, None])
+    # the roundings of the gated row and the output, as in check_experts
+    assert (out.double() - ref).norm() <= 1.25 * 2 ** 0.5 * 2.0 ** -8 / 3 ** 0.5 * ref.norm()
+    assert (out[(ids < 0).all(1)] == 0).all()
+
+
 def test_experts_model_width(oracle_mod):
     """6144 columns, 1,024 hidden: one token's six experts, and a step of 20 tokens."""
     x, ids, w, w_in, w_out = expert_inputs(50, 20, 6, 8, 6144, 1024)
