@@ -274,11 +274,13 @@ __device__ __forceinline__ void make_small_plan(const Shared &c, int tile_tokens
 // and read back, cost a prompt of 4,096 tokens 937 us against 887. 11 bits beside the scale are off
 // by 2^-11 at most, an eighth of the rounding of the gated row and of the output to bf16; the
 // tokens' sums are fp32.)
-template <int kTokens, bool kSmall = false>
+template <int kTokens, bool kSmall = false, bool kTall = false>
 struct EX {
+  static constexpr int SETS = kTall ? 2 : 1;           // accumulators per tile, of 256 M rows per pair
+  static constexpr int ACCS = 2 / SETS;                // tiles in TMEM at a time
   static constexpr int BK = 64;                        // K per stage: 128 bytes of a token row
   static constexpr int BOX = 64 * BK * 2;              // 64 columns x 64 K rows of weights: 8 KB
-  static constexpr int A_STAGE = 2 * BOX;              // this CTA's 128 M rows
+  static constexpr int A_STAGE = SETS * 2 * BOX;       // this CTA's 128 M rows of each set
   static constexpr int B_STAGE = kTokens / 2 * BK * 2; // this CTA's half of the tokens
   static constexpr int EPI_GROUPS = 2, EPI_WARPS = 4 * EPI_GROUPS;
   static constexpr int STG_TOKENS = 32;
@@ -303,7 +305,6 @@ struct EX {
   static constexpr int GATHER_WARPS = kTokens > 64 ? 8 : 2;
   static constexpr int THREADS = 32 * (2 + EPI_WARPS);
   static constexpr int THREADS_GATE = THREADS + 32 * GATHER_WARPS;
-  static constexpr uint32_t ACC_STRIDE = kTokens;
   static constexpr uint32_t TMEM_COLS = 2 * kTokens < 32 ? 32 : 2 * kTokens;
   static_assert(kTokens % 32 == 0 && kTokens <= 256 && (TMEM_COLS & (TMEM_COLS - 1)) == 0, "token tile");
   static_assert(B_STAGE % 1024 == 0 && STAGES >= 4 && STAGES <= 24, "stages");
@@ -415,15 +416,19 @@ __device__ __forceinline__ void small_sum(const Shared &c, const float *y, int d
 
 // kSmall: the gate's kernel makes the plan, the down product's kernel the tokens' sums (Shared).
 // kSplit: K in parts (of the gate's kernel).
-template <int kTokens, bool kGate, bool kSmall, bool kSplit>
-__global__ void __launch_bounds__(kGate ? EX<kTokens, kSmall>::THREADS_GATE : EX<kTokens, kSmall>::THREADS, 1)
+// kTall: tiles of twice the columns (of the gate's kernel), with both halves of TMEM for one tile. What
+// bounds wide tiles is the loads from L2 (12 TB/s, 6.7 GB for 4,096 tokens of 6 slots, 6144 x 2 x
+// 1024, the tensor pipe 58 % active); a tall tile needs three quarters of the bytes, and more than
+// makes up for an epilogue that nothing runs under where K is long (the whole call: 924 us to 863).
+template <int kTokens, bool kGate, bool kSmall, bool kSplit, bool kTall>
+__global__ void __launch_bounds__(kGate ? EX<kTokens, kSmall, kTall>::THREADS_GATE : EX<kTokens, kSmall, kTall>::THREADS, 1)
     experts_product_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
                            const __grid_constant__ CUtensorMap xmap8, const int *__restrict__ n_tiles,
                            const TokenTile *tiles, const int *token, int K, int cols, void *out, const Shared shared,
                            uint32_t *err) {
-  using X = EX<kTokens, kSmall>;
+  using X = EX<kTokens, kSmall, kTall>;
   constexpr int STAGES = X::STAGES, BK = X::BK;
-  constexpr int COLS = kGate ? 64 : 128;  // columns of the output per CTA
+  constexpr int SET_COLS = kGate ? 64 : 128, COLS = SET_COLS * X::SETS;  // columns of the output per CTA
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t *smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -505,9 +510,13 @@ __global__ void __launch_bounds__(kGate ? EX<kTokens, kSmall>::THREADS_GATE : EX
           if (leader) mbar_arrive_expect_tx(full(stage), bytes);
           const uint32_t fb = mapa_shared(full(stage), 0);
           const uint32_t a_dst = smem_addr(smem + stage * X::A_STAGE);
-          // kGate: the gate's box, then the up box `cols` further on
-          tma_load_3d_pair(a_dst, &wmap, col, kb * BK, tt.expert, fb);
-          tma_load_3d_pair(a_dst + X::BOX, &wmap, col + (kGate ? cols : 64), kb * BK, tt.expert, fb);
+#pragma unroll
+          for (int set = 0; set < X::SETS; ++set) {
+            // kGate: the gate's box, then the up box `cols` further on
+            const int c0 = col + SET_COLS * set;
+            tma_load_3d_pair(a_dst + 2 * set * X::BOX, &wmap, c0, kb * BK, tt.expert, fb);
+            tma_load_3d_pair(a_dst + (2 * set + 1) * X::BOX, &wmap, c0 + (kGate ? cols : 64), kb * BK, tt.expert, fb);
+          }
           if (!kGate) {
             // rows past the tile are the next expert's, or zeros past the last: computed, not stored
             const uint32_t b_dst = smem_addr(smem + X::OFF_B + stage * X::B_STAGE);
@@ -534,12 +543,12 @@ __global__ void __launch_bounds__(kGate ? EX<kTokens, kSmall>::THREADS_GATE : EX
       uint32_t phase = 0, i = 0;
       bool ok = true;
       for (int64_t t = blockIdx.x >> 1; ok && t < total; t += step, ++i) {
-        const uint32_t acc = i & 1u, use = i >> 1;
+        const uint32_t acc = i % X::ACCS, use = i / X::ACCS;
         const uint32_t idesc = idesc_bf16_f32(256, (uint32_t)token_tile(t).width, 0, 1);
         const int kb0 = kb_begin(t), kb1 = kb_end(t);
         if (!__all_sync(kAll, mbar_wait(tempty(acc), (use & 1u) ^ 1u, err))) break;
         tc_fence_after();
-        const uint32_t d = tmem_base + acc * X::ACC_STRIDE;
+        const uint32_t d = tmem_base + acc * kTokens;
         for (int kb = kb0; kb < kb1; ++kb) {
           if (!__all_sync(kAll, mbar_wait(full(stage), phase, err))) { ok = false; break; }
           tc_fence_after();
@@ -547,12 +556,15 @@ __global__ void __launch_bounds__(kGate ? EX<kTokens, kSmall>::THREADS_GATE : EX
           const uint32_t b0 = smem_addr(smem + X::OFF_B + stage * X::B_STAGE);
           if (elect_one()) {
 #pragma unroll
-            for (int k = 0; k < BK / 16; ++k) {
-              // weights: MN-major, 64-column boxes BOX apart, 8 K-rows 1024 B apart, 16 (2 KB) per step
-              const uint64_t adesc = smem_desc(a0 + 2048u * k, (uint32_t)X::BOX, 1024u, kSwizzle128B);
-              // tokens: K-major, 8-row groups 1024 B apart, 32 B per step
-              const uint64_t bdesc = smem_desc(b0 + 32u * k, 16u, 1024u, kSwizzle128B);
-              tc_mma_f16_pair(d, adesc, bdesc, idesc, kb > kb0 || k > 0 ? 1u : 0u);
+            for (int set = 0; set < X::SETS; ++set) {
+#pragma unroll
+              for (int k = 0; k < BK / 16; ++k) {
+                // weights: MN-major, 64-column boxes BOX apart, 8 K-rows 1024 B apart, 16 (2 KB) per step
+                const uint64_t adesc = smem_desc(a0 + 2 * set * X::BOX + 2048u * k, (uint32_t)X::BOX, 1024u, kSwizzle128B);
+                // tokens: K-major, 8-row groups 1024 B apart, 32 B per step
+                const uint64_t bdesc = smem_desc(b0 + 32u * k, 16u, 1024u, kSwizzle128B);
+                tc_mma_f16_pair(d + set * kTokens, adesc, bdesc, idesc, kb > kb0 || k > 0 ? 1u : 0u);
+              }
             }
             tc_commit_pair_both(empty(stage), 3);
           }
@@ -614,13 +626,17 @@ __global__ void __launch_bounds__(kGate ? EX<kTokens, kSmall>::THREADS_GATE : EX
     uint32_t i = 0;
     bool ok = true;
     for (int64_t t = blockIdx.x >> 1; t < total; t += step, ++i) {
-      const uint32_t acc = i & 1u, use = i >> 1;
+      const uint32_t acc = i % X::ACCS, use = i / X::ACCS;
       const TokenTile tt = token_tile(t);
-      const int col = column(t);
+      const int first_col = column(t);
       ok = group_bar_and(1 + group, ok && mbar_wait(tfull(acc), use & 1u, err));
       tc_fence_after();
-      const uint32_t tb = tmem_base + ((uint32_t)(32 * quad) << 16) + acc * X::ACC_STRIDE;
-      for (int c = X::STG_TOKENS * group; ok && c < tt.width; c += X::STG_TOKENS * X::EPI_GROUPS) {
+      // chunks of both sets, the sets one after the other
+      const int per_set = (tt.width + X::STG_TOKENS - 1) / X::STG_TOKENS;
+      for (int n = group; ok && n < per_set * X::SETS; n += X::EPI_GROUPS) {
+        const int set = X::SETS > 1 && n >= per_set ? 1 : 0, c = X::STG_TOKENS * (n - set * per_set);
+        const int col = first_col + SET_COLS * set;
+        const uint32_t tb = tmem_base + ((uint32_t)(32 * quad) << 16) + (acc + set) * kTokens;
         // 32 tokens (16 where the tile ends) of this lane's column into the staging rows
         const bool wide = tt.width - c >= 32;
         uint32_t v[2][16];
@@ -702,12 +718,12 @@ __global__ void __launch_bounds__(kGate ? EX<kTokens, kSmall>::THREADS_GATE : EX
       if (lane == 0) mbar_arrive_remote(mapa_shared(tempty(acc), 0));
       if (kSplit) {
         if (last_of(splits, shared.counters + 2 * ((K + 255) / 256) + 2 * tile_of(t) + rank, last))
-          join_splits<kTokens>(shared, static_cast<__nv_bfloat16 *>(out), tile_of(t), (int)rank, tt, cols, col);
+          join_splits<kTokens>(shared, static_cast<__nv_bfloat16 *>(out), tile_of(t), (int)rank, tt, cols, first_col);
       }
       if (kSmall && !kGate) {
         // these columns of all tokens, when every token tile has been through them
         if (last_of(token_tiles, shared.counters + 2 * (t % n_ct) + rank, last))
-          small_sum(shared, static_cast<const float *>(out), cols, col);
+          small_sum(shared, static_cast<const float *>(out), cols, first_col);
       }
     }
     if (kSmall && !kGate && token_tiles == 0)  // no token has an expert: zeros
@@ -845,20 +861,21 @@ struct Call {
   int dim, hidden;
   void *h, *y;
   Shared shared;
+  bool tall;
   int64_t max_tiles;
   uint32_t *err;
   int num_sms;
   cudaStream_t stream;
 };
 
-template <int kTokens, bool kGate, bool kSmall, bool kSplit>
+template <int kTokens, bool kGate, bool kSmall, bool kSplit, bool kTall = false>
 cudaError_t launch_product(const Call &c) {
-  using X = EX<kTokens, kSmall>;
+  using X = EX<kTokens, kSmall, kTall>;
   static std::atomic<bool> attr[256];
-  const auto kernel = experts_product_kernel<kTokens, kGate, kSmall, kSplit>;
+  const auto kernel = experts_product_kernel<kTokens, kGate, kSmall, kSplit, kTall>;
   const cudaError_t e = set_smem_attr_once(kernel, X::SMEM_BYTES, attr);
   if (e != cudaSuccess) return e;
-  const int cols = kGate ? c.hidden : c.dim, per_pair = kGate ? 128 : 256;
+  const int cols = kGate ? c.hidden : c.dim, per_pair = (kGate ? 128 : 256) * X::SETS;
   const int64_t work = c.max_tiles * ((cols + per_pair - 1) / per_pair) * (kGate ? c.shared.splits : 1);
   const int64_t pairs = c.num_sms / 2 > 0 ? c.num_sms / 2 : 1;
   cudaLaunchConfig_t cfg = {};
@@ -884,7 +901,11 @@ cudaError_t launch_product(const Call &c) {
 template <int kTokens, bool kSmallGate, bool kSmallDown>
 cudaError_t launch_products(const Call &c, int *launches) {
   cudaError_t e;
-  if constexpr (!kSmallGate)
+  if constexpr (kTokens == 256)
+    e = c.tall                ? launch_product<kTokens, true, false, false, true>(c)
+        : c.shared.splits > 1 ? launch_product<kTokens, true, false, true>(c)
+                              : launch_product<kTokens, true, false, false>(c);
+  else if constexpr (!kSmallGate)
     e = c.shared.splits > 1 ? launch_product<kTokens, true, false, true>(c) : launch_product<kTokens, true, false, false>(c);
   else
     e = launch_product<kTokens, true, true, false>(c);
@@ -979,6 +1000,8 @@ cudaError_t launch_experts(const void *x, int64_t n_tokens, const int32_t *ids, 
       !row_map(&c.out_h, enc, c.h, n_slots, w.hidden, 32) || !row_map(&c.out_h8, enc, c.h, n_slots, w.hidden, 8))
     return cudaErrorInvalidValue;
   c.max_tiles = cf.max_tiles;
+  // tall tiles where they still make several rounds over the pairs, and K is 32 blocks or more
+  c.tall = cf.max_tiles * ((w.hidden + 255) / 256) >= 3 * kPairs && w.dim >= 2048;
   cudaError_t e = cudaSuccess;
   // the splits' counters are cleared by the plan's kernel
   if (cf.small && cf.splits == 1) return launch_products<32, true, true>(c, launches);

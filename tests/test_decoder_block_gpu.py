@@ -327,9 +327,10 @@ def test_experts(n, slots, e, d, h, oracle_mod):
     check_experts(*expert_inputs(n + d, n, slots, e, d, h), oracle_mod)
 
 
-@pytest.mark.parametrize("n,slots,e,d,h", [(30000, 5, 3, 16, 8), (20000, 6, 32, 16, 8), (1500, 1, 1000, 16, 8)])
+@pytest.mark.parametrize("n,slots,e,d,h", [(30000, 5, 3, 16, 8), (20000, 6, 32, 16, 8), (1500, 1, 1000, 16, 8),
+                                           (14000, 2, 5, 2056, 600)])
 def test_experts_many_slots(n, slots, e, d, h):
-    """Plans of several blocks and batches: against the formula in fp64, expert by expert."""
+    """Plans of several blocks and batches, tiles of twice the columns: against the formula in fp64, expert by expert."""
     x, ids, w, w_in, w_out = expert_inputs(n, n, slots, e, d, h, empty=0.1)
     out = run_experts(x, ids, w, w_in, w_out)
     ref = torch.zeros((n, d), dtype=torch.float64, device=DEV)
