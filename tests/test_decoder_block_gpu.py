@@ -251,6 +251,40 @@ def test_route_masks(sigmoid, oracle_mod):
         assert w[7, 0] == 1.0 and (w[7, 1:] == 0).all()
 
 
+@pytest.mark.parametrize("sigmoid", [True, False])
+def test_route_bias_without_a_value(sigmoid, oracle_mod):
+    """NaN and -inf in the bias keep an expert out, +inf puts it first (several by index)."""
+    g = torch.Generator(device=DEV).manual_seed(9)
+    logits = torch.randn((20, 48), generator=g, device=DEV)
+    bias = 0.1 * torch.randn(48, generator=g, device=DEV)
+    bias[3] = bias[17] = float("nan")
+    bias[20:30] = -float("inf")
+    bias[40] = bias[12] = float("inf")
+    for groups, kept in ((1, 1), (6, 4)):
+        ids, _ = check_route(logits, 5, oracle_mod, bias, 0, sigmoid, groups, kept)
+        assert (ids[:, :2] == [12, 40]).all()
+    bias[:] = float("nan")
+    ids, w = check_route(logits, 5, oracle_mod, bias, 0, sigmoid)
+    assert (ids == -1).all() and (w == 0).all()
+
+
+@pytest.mark.parametrize("k,shared", [(1, 31), (31, 1), (32, 0), (12, 0)])
+def test_route_all_slots(k, shared, oracle_mod):
+    g = torch.Generator(device=DEV).manual_seed(10)
+    logits = torch.randn((40, 64 + shared), generator=g, device=DEV)
+    check_route(logits, k, oracle_mod, 0.1 * torch.randn(64, generator=g, device=DEV), shared)
+
+
+def test_no_rows_on_the_gpu():
+    e = lambda *shape, dtype=F32: torch.empty(shape, dtype=dtype, device=DEV)  # noqa: E731
+    dmel.dmel_add_rmsnorm(e(0, 64), e(64), e(0, 64), residual=e(0, 64))
+    dmel.dmel_route(e(0, 8), e(0, 2, dtype=torch.int32), e(0, 2))
+    assert dmel.dmel_experts_workspace_size(0, 2, 4, 64, 32) == 0
+    dmel.dmel_experts(e(0, 64, dtype=BF16), e(0, 2, dtype=torch.int32), e(0, 2), e(4, 64, 64, dtype=BF16),
+                      e(4, 32, 64, dtype=BF16), e(0, 64, dtype=BF16), None)
+    assert dmel.dmel_last_launch_count() == 0
+
+
 def test_route_small_scores_keep_their_ratios(oracle_mod):
     """Sigmoids far below fp32's range: the renormalised weights are those of the formula."""
     logits = torch.tensor([[-200.0, -201.0, -203.0, -260.0], [-90.0, -89.0, -95.0, -88.5]], device=DEV)
@@ -322,7 +356,9 @@ def check_experts(x, ids, w, w_in, w_out, oracle_mod):
     (1100, 4, 2, 64, 520), (3, 2, 1024, 24, 16), (171, 3, 40, 72, 40), (64, 1, 1, 64, 264), (65, 1, 1, 64, 72),
     (16, 4, 33, 520, 136), (32, 2, 3, 264, 72), (13, 5, 9, 520, 136),
     # the first product's K in parts: 2, 4, 4, 2, 3
-    (5, 2, 3, 2056, 72), (40, 2, 2, 4104, 136), (1, 1, 2, 4096, 64), (700, 1, 1, 2200, 200), (130, 3, 5, 3080, 264)])
+    (5, 2, 3, 2056, 72), (40, 2, 2, 4104, 136), (1, 1, 2, 4096, 64), (700, 1, 1, 2200, 200), (130, 3, 5, 3080, 264),
+    # the widest
+    (3, 2, 2, 65536, 8), (3, 2, 2, 8, 65536)])
 def test_experts(n, slots, e, d, h, oracle_mod):
     check_experts(*expert_inputs(n + d, n, slots, e, d, h), oracle_mod)
 

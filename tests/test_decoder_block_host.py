@@ -165,6 +165,39 @@ def test_binding_refuses_what_c_cannot_see(lib):
             dmel.dmel_experts(*a)
 
 
+def test_binding_runs_on_the_tensors_device(monkeypatch):
+    """A call on device 1 while device 0 is current: made with device 1 current, on its current stream or on a
+    stream of its own, never on another device's."""
+    import contextlib
+    current = [0]
+
+    @contextlib.contextmanager
+    def on(index):
+        current.append(index)
+        yield
+        current.pop()
+
+    monkeypatch.setattr(torch.cuda, "device", on)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: current[-1], raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda d: 1000 + d, raising=False)
+    calls = []
+
+    def entry(*args):
+        calls.append((current[-1], args))
+        return dmel.DMEL_OK
+
+    dmel._run_on(1, None, "call", entry, 5)
+    dmel._run_on(0, None, "call", entry, 6)
+
+    class Stream:
+        device_index, device, cuda_stream = 1, "cuda:1", 77
+
+    dmel._run_on(1, Stream, "call", entry, 7)
+    assert calls == [(1, (5, 1001)), (0, (6, 1000)), (1, (7, 77))] and current == [0]
+    with pytest.raises(dmel.DmelError, match="a stream of cuda:1"):
+        dmel._run_on(0, Stream, "call", entry, 8)
+
+
 # ------------------------------------------------------------------------------ pins of the oracle
 
 def test_oracle_add_rmsnorm_closed_form(oracle_mod):
