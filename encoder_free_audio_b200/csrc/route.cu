@@ -4,16 +4,18 @@
 //
 // One warp per token: lane l holds experts l, l + 32, ... in registers, so a row is read once,
 // coalesced, and no value leaves the warp before the ids and weights are written. With many tokens
-// the kernel is bound by its instructions (about 850 per token of 256 experts, 72 % of the issue slots), not by the row's
-// 1 KB: each lane orders its experts by a network of comparisons on values whose last bits give way
-// to the expert's place, and top_k rounds take the largest head of the 32 lanes with one reduction
-// each. (8 lanes per token with their best 16 merged, so that four tokens share the rounds, needs
-// more registers than fit beside enough warps: 48 us for 24,000 tokens where this takes 27.)
+// the kernel is bound by its instructions, not by the row's 1 KB: each lane orders its experts by a
+// network of comparisons on values whose last bits give way to the expert's place, and top_k rounds
+// take the largest head of the 32 lanes with one reduction each. (8 lanes per token with their best
+// 16 merged, so that four tokens share the rounds, needs more registers than fit beside enough warps:
+// 48 us for 24,000 tokens of 256 experts, where this takes 23.)
 //
-// The order is that of 64-bit arithmetic, although the scores are fp32 and cut short: each round
-// also checks that its winner is above the next by more than the two can be off. A token where it
-// is not (about one in five hundred of ordinary logits) is chosen again in fp64, which takes that warp
-// 4 to 8 us: without such tokens the same call takes 19 us.
+// The order is that of 64-bit arithmetic, although the scores are fp32 and cut short: the lanes check
+// that each winner is above the next by more than the two can be off. A token where one is not (about
+// one in five hundred of ordinary logits) has the winners and what is near the last of them ordered
+// by their scores in fp64, one candidate a lane: 1.4 us with sigmoids, 3.2 with a softmax, whose sum
+// is wanted too. All experts are chosen again in fp64 (7 to 9 us) only where two groups are that near
+// or more than 32 candidates are. Without such tokens the 24,000 take 20.6 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math_constants.h>
@@ -93,6 +95,11 @@ __device__ __forceinline__ float warp_max(float v) {
   asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
   return m;
 }
+__device__ __forceinline__ double warp_max(double v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(kAll, v, o));
+  return v;
+}
 template <typename F>
 __device__ __forceinline__ F warp_sum(F v) {
 #pragma unroll
@@ -170,13 +177,8 @@ __device__ __forceinline__ unsigned keep_groups(const F *v, const Settings &q, F
   }
   const bool in = lane < groups && before < q.r.topk_groups;
   F lo = in ? rated : -(F)kNone, hi = in ? (F)kNone : rated;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    lo = min(lo, __shfl_xor_sync(kAll, lo, o));
-    hi = max(hi, __shfl_xor_sync(kAll, hi, o));
-  }
-  *worst = lo;
-  *best = hi;
+  *worst = -warp_max(-lo);
+  *best = warp_max(hi);
   return __ballot_sync(kAll, in);
 }
 
@@ -187,8 +189,8 @@ __device__ __forceinline__ unsigned long long order_of(double v) {
 }
 
 // The choice in fp64: the id of slot `lane`, -1 for none. `top` is the token's largest logit, v the
-// warp's shared memory. Apart from the kernel, since one token in hundreds comes here; written for
-// a short way through, since the last of them ends the launch.
+// warp's shared memory. Apart from the kernel, since few tokens come here; written for a short way
+// through, since the last of them may end the launch.
 template <typename T, int EPL>
 __device__ __noinline__ int choose_fp64(const T *row, const float *bias, const Settings &q, float top, double *v) {
   const dmel_router &r = q.r;
@@ -259,14 +261,52 @@ __device__ __noinline__ int choose_fp64(const T *row, const float *bias, const S
   return my_id;
 }
 
+// The n <= 32 candidates that the lanes hold an id of, in order: the id of place `lane`. They compare as
+// logits, or with a bias as scores in fp64. `top` is the token's largest logit. Short code rather than
+// overlapped: an SM that comes here rarely waits for the instructions (three exponentials at a time
+// take as long).
+template <typename T>
+__device__ __noinline__ int order_fp64(const T *row, const float *bias, const dmel_router &r, float top, int id, int n) {
+  const int lane = threadIdx.x & 31;
+  const bool softmax = r.scoring == DMEL_ROUTE_SOFTMAX;
+  double x = id >= 0 ? (double)clean(logit(row + id)) : (double)kNone;
+  if (bias) {
+    const int end = softmax ? r.n_experts + r.n_shared : 0;
+    double own = 0.0, z = 0.0;
+#pragma unroll 1
+    for (int e = lane - 32; e < end; e += 32) {  // first the candidate, then the token's sum
+      const double l = e < 0 ? x : (double)clean(logit(row + e));
+      const double a = exp(softmax ? l - (double)top : -l);
+      if (e < 0) own = a;
+      else z += a;
+    }
+    __syncwarp();
+    z = softmax ? warp_sum(z) : 1.0 + own;
+    x = (softmax ? own : 1.0) / z + (double)__ldg(bias + max(id, 0));
+  }
+  int before = 0;
+  for (int j = 0; j < n; ++j) {
+    const double o = __shfl_sync(kAll, x, j);
+    const int other = __shfl_sync(kAll, id, j);
+    before += other >= 0 && (o > x || (o == x && other < id));
+  }
+  int mine = -1;
+  for (int j = 0; j < n; ++j) {
+    const int place = __shfl_sync(kAll, before, j), other = __shfl_sync(kAll, id, j);
+    if (place == lane && other >= 0) mine = other;
+  }
+  return mine;
+}
+
 // kScored: the choice compares scores (a bias, or groups), else the logits themselves.
 template <typename T, int EPL, bool kScored, bool kGroups>
 __global__ void __launch_bounds__(32 * kWarps, 7) route_kernel(const T *__restrict__ logits, int64_t n_tokens,
-                                                            const float *__restrict__ bias, const Settings q,
+                                                            const float *__restrict__ bias, const __grid_constant__ Settings q,
                                                             int32_t *__restrict__ ids, float *__restrict__ weights) {
   const dmel_router &r = q.r;
   const int lane = threadIdx.x & 31, E = r.n_experts, S = r.n_shared, K = r.top_k;
   const int cols = E + S, slots = K + S;
+  const unsigned lanes_below = (1u << lane) - 1u;
   const bool sigmoid = r.scoring == DMEL_ROUTE_SIGMOID;
   extern __shared__ double smem[];  // with groups: a token's values per warp
   double *const wide = smem + (threadIdx.x >> 5) * q.warp_doubles;
@@ -338,26 +378,66 @@ __global__ void __launch_bounds__(32 * kWarps, 7) route_kernel(const T *__restri
 #pragma unroll
     for (int i = 0; i < EPL; ++i) key[i] = key_of<EPL>(v[i], i);
     sort_down<EPL>(key);
-    int my_id = -1;  // of slot `lane`
-    int last = 0;
-    float last_v = 0.0f;
-    for (int k = 0; k <= K; ++k) {  // the round after the last only checks the margin
-      const float best = warp_max(key[0]);
-      if (!(best > kNone)) break;  // nothing left
-      const int owner = __ffs(__ballot_sync(kAll, key[0] == best)) - 1;
-      const int idx = owner + 32 * place_of<EPL>(best);
-      const float b = value_of<EPL>(best);
-      if (lane == k) my_id = idx;
-      // nearer than they may be off; two experts alike are a tie, which goes by index here as well
-      if (k > 0 && !(last_v - b > margin<EPL>(bias ? off : 0.0f, last_v, b)) &&
-          !(at(last) == at(idx) && (!bias || __ldg(bias + last) == __ldg(bias + idx))))
-        unsure = true;
-      last = idx;
-      last_v = b;
-      if (lane == owner) {
+    // top_k rounds: the largest head, the lowest lane among equals; slot k's key and lanes stay in lane k
+    float mine = kNone, best = kNone;
+    unsigned holders = 0, heads = 0;
+    auto round = [&](int k) {
+      best = warp_max(key[0]);
+      const bool held = key[0] == best;
+      heads = __ballot_sync(kAll, held);
+      if (lane == k) {
+        mine = best;
+        holders = heads;
+      }
+      return held && !(heads & lanes_below);
+    };
+    auto drop = [&](bool owner) {
+      if (owner) {
 #pragma unroll
         for (int i = 0; i + 1 < EPL; ++i) key[i] = key[i + 1];
         key[EPL - 1] = kNone;
+      }
+    };
+    auto expert_of = [&](float k, unsigned lanes) { return __ffs(lanes) - 1 + 32 * place_of<EPL>(k); };
+    const float key_off = bias ? off : 0.0f;
+    auto near = [&](float a, float b) {  // keys a >= b that may stand the other way round in 64 bits
+      const float x = value_of<EPL>(a), y = value_of<EPL>(b);
+      return b > kNone && !(x - y > margin<EPL>(key_off, x, y));
+    };
+    auto alike = [&](int e, int f) { return at(e) == at(f) && (!bias || __ldg(bias + e) == __ldg(bias + f)); };
+    for (int k = 0; k < K; ++k) {
+      const bool owner = round(k);
+      if (!(best > kNone)) break;  // nothing left
+      drop(owner);
+    }
+    best = warp_max(key[0]);  // the first that is not chosen
+    int my_id = lane < K && mine > kNone ? expert_of(mine, holders) : -1;  // of slot `lane`
+    const float next = __shfl_down_sync(kAll, mine, 1);
+    const unsigned close = __ballot_sync(kAll, lane < K && near(mine, lane == K - 1 ? best : next));
+    if (close) {
+      // Two experts alike are a tie, which the keys settle by index; with the last of the chosen they
+      // do where no expert that is left is near it and not alike.
+      const bool edge = (close >> (K - 1)) & 1u;
+      const float least = __shfl_sync(kAll, mine, (K - 1) & 31);
+      const int least_id = __shfl_sync(kAll, my_id, (K - 1) & 31), next_id = __shfl_down_sync(kAll, my_id, 1);
+      bool open = lane < K - 1 && ((close >> lane) & 1u) && !alike(my_id, next_id);
+      if (edge) {
+#pragma unroll
+        for (int i = 0; i < EPL; ++i)
+          if (near(least, key[i])) open |= !alike(least_id, lane + 32 * place_of<EPL>(key[i]));
+      }
+      if (__any_sync(kAll, open)) {
+        int n = K;  // the chosen, and all that are near the last of them
+        if (edge) {
+          for (; n < 32; ++n) {
+            const bool owner = round(n);
+            if (!near(least, best)) break;
+            drop(owner);
+          }
+          my_id = lane < n ? expert_of(mine, holders) : -1;
+          if (n == 32) unsure = near(least, warp_max(key[0])) || unsure;
+        }
+        if (!unsure) my_id = order_fp64(row, bias, r, top, my_id, n);
       }
     }
     if (unsure) my_id = choose_fp64<T, EPL>(row, bias, q, top, wide);

@@ -418,7 +418,7 @@ dmel_status dmel_route(const void *logits, int64_t n_tokens, dmel_dtype dtype, c
  * operand), each expert's output row to 11 bits beside a scale per 128 columns, and the token's
  * fp32 sum to bf16.
  * Results do not depend on how tokens are batched, up to fp32 summation inside the tensor cores.
- * n_tokens * slots at most 2^30. Asynchronous on stream; two launches up to 64 slots, then four. */
+ * n_tokens * slots at most 2^30. Asynchronous on stream; two to four launches, by the number of slots. */
 typedef struct {
   int n_experts;     /* 1 .. 1024 */
   int dim;           /* model width, a positive multiple of 8, at most 65536 */

@@ -222,6 +222,40 @@ def test_route_values_fp32_cannot_tell_apart(sigmoid, oracle_mod):
 
 
 @pytest.mark.parametrize("sigmoid", [True, False])
+@pytest.mark.parametrize("e,k", [(24, 4), (24, 24), (40, 31), (40, 32), (300, 6)])
+def test_route_few_near_one_another(e, k, sigmoid, oracle_mod):
+    """As above, with up to 24 experts near one another and the others far below, or all in pairs and threes."""
+    r = np.random.default_rng(e + k)
+    for size in (2, 3, 24):
+        base = r.standard_normal(e).astype(np.float32)
+        rows = np.repeat(base[None], 50, 0)
+        steps = np.spacing(rows) * r.integers(-1, 2, rows.shape)
+        rows = np.where(r.random(rows.shape) < 0.5, rows + steps.astype(np.float32), rows)
+        l = base.astype(np.float64)
+        s = 1 / (1 + np.exp(-l)) if sigmoid else np.exp(l) / np.exp(l).sum()
+        height = -0.25 * (np.arange(e) // size)  # sets of `size` experts at the same height
+        bias = (height[r.permutation(e)] - s).astype(np.float32)
+        check_route(torch.from_numpy(rows).to(DEV), k, oracle_mod, torch.from_numpy(bias).to(DEV), sigmoid=sigmoid)
+
+
+@pytest.mark.parametrize("e,groups", [(30, 1), (256, 1), (256, 8), (1000, 1)])
+@pytest.mark.parametrize("near", [3, 8, 40])
+def test_route_ties_among_near_logits(e, groups, near, oracle_mod):
+    """Equal logits at the edge of the choice with others a unit or two in the last place away; no bias, and
+    a bias that is the same for all of them."""
+    r = np.random.default_rng(e + near)
+    rows = r.standard_normal((60, e)).astype(np.float32)
+    for row in rows:
+        at = r.permutation(e)[:near]
+        level = np.sort(row)[-6]
+        row[at] = level + np.spacing(level) * r.integers(-1, 2, at.size).astype(np.float32)
+    logits = torch.from_numpy(rows).to(DEV)
+    for bias in (None, torch.full((e,), 0.125, device=DEV)):
+        for sigmoid in (True, False):
+            check_route(logits, 6, oracle_mod, bias, 0, sigmoid, groups, (groups + 1) // 2)
+
+
+@pytest.mark.parametrize("sigmoid", [True, False])
 def test_route_masks(sigmoid, oracle_mod):
     """-inf, the types' lowest values, NaN and +inf; rows with fewer experts than slots, and with none."""
     inf, nan, low = float("inf"), float("nan"), torch.finfo(F32).min
