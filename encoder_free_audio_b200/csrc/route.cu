@@ -8,14 +8,14 @@
 // network of comparisons on values whose last bits give way to the expert's place, and top_k rounds
 // take the largest head of the 32 lanes with one reduction each. (8 lanes per token with their best
 // 16 merged, so that four tokens share the rounds, needs more registers than fit beside enough warps:
-// 48 us for 24,000 tokens of 256 experts, where this takes 23.)
+// 48 us for 24,000 tokens of 256 experts, where this takes 21.)
 //
 // The order is that of 64-bit arithmetic, although the scores are fp32 and cut short: the lanes check
 // that each winner is above the next by more than the two can be off. A token where one is not (about
 // one in five hundred of ordinary logits) has the winners and what is near the last of them ordered
-// by their scores in fp64, one candidate a lane: 1.4 us with sigmoids, 3.2 with a softmax, whose sum
-// is wanted too. All experts are chosen again in fp64 (7 to 9 us) only where two groups are that near
-// or more than 32 candidates are. Without such tokens the 24,000 take 20.6 us.
+// by their scores in fp64, one candidate a lane: 1.5 us with sigmoids, 2.7 with a softmax, whose sum
+// is wanted too. All experts are chosen again in fp64 (6 to 8 us) only where two groups are that near
+// or more than 32 candidates are.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math_constants.h>
@@ -69,13 +69,10 @@ __device__ __forceinline__ float value_of(float k) {  // cut towards -inf, by le
 // softmax's, with its sum of up to 1,056 terms by pairs: 1.8e-6 of the token's largest score, 1 / z.
 constexpr float kSigmoidOff = 3.5e-7f, kSoftmaxOff = 2e-6f;
 
-// How far apart two choice values must be for their keys, a above b, to order them as 64-bit
-// arithmetic does: twice the score's error `off` (0 for logits), the rounding of the sums with the
-// bias, and what key_of<N> may have cut off b.
-template <int N>
-__device__ __forceinline__ float margin(float off, float a, float b) {
-  return 2.0f * off + (N + 2) * 1.2e-7f * fmaxf(fabsf(a), fabsf(b));
-}
+// Two choice values' keys, a above b, stand as in 64-bit arithmetic where they are further apart than
+// twice the scores' error (0 for logits) and this share of the larger: the rounding of the sums with
+// the bias, and what key_of<N> may have cut off b.
+__host__ __device__ constexpr float cut_of(int N) { return (N + 2) * 1.2e-7f; }
 
 // exp and 1 / x on the special-function unit (a few ulps, results below the normal range zero).
 __device__ __forceinline__ float fast_exp(float x) {
@@ -261,28 +258,74 @@ __device__ __noinline__ int choose_fp64(const T *row, const float *bias, const S
   return my_id;
 }
 
-// The n <= 32 candidates that the lanes hold an id of, in order: the id of place `lane`. They compare as
-// logits, or with a bias as scores in fp64. `top` is the token's largest logit. Short code rather than
-// overlapped: an SM that comes here rarely waits for the instructions (three exponentials at a time
-// take as long).
+// An expert's score in fp32, of its logit l; z: the softmax's sum.
+__device__ __forceinline__ float score_of(bool sigmoid, float l, float top, float inv_z) {
+  return sigmoid ? fast_rcp(1.0f + fast_exp(-l)) : __fmul_rn(fast_exp(l - top), inv_z);
+}
+
+// The experts chosen in fp32 (lane k: slot k's id) where `close` has a bit for each slot whose key is
+// near the next one's (the last slot's: the next that is not chosen), put right: the id of slot
+// `lane`, or kTooMany in all lanes. `top` is the token's largest logit, z the softmax's sum, `least` the
+// last slot's value; values a >= b are near within off + cut max(|a|, |b|). Two experts alike are a tie,
+// which the keys settle by index; with the last of the chosen they do where no other expert is near it
+// and not alike. Else the chosen, with all that are near the last of them, are ordered as logits, or
+// with a bias as scores in fp64, one candidate a lane. Short code rather than overlapped: an SM that
+// comes here rarely waits for the instructions.
+constexpr int kTooMany = -2;  // candidates for the lanes of a warp
+
 template <typename T>
-__device__ __noinline__ int order_fp64(const T *row, const float *bias, const dmel_router &r, float top, int id, int n) {
-  const int lane = threadIdx.x & 31;
+__device__ __noinline__ int settle(const T *row, const float *bias, const Settings &q, float top, float z, unsigned kept,
+                                   float least, float off, float cut, unsigned close, int id, int *list) {
+  const dmel_router &r = q.r;
+  const int lane = threadIdx.x & 31, E = r.n_experts, K = r.top_k;
   const bool softmax = r.scoring == DMEL_ROUTE_SOFTMAX;
+  auto alike = [&](int e, int f) {
+    return clean(logit(row + e)) == clean(logit(row + f)) && (!bias || __ldg(bias + e) == __ldg(bias + f));
+  };
+  const int next_id = __shfl_down_sync(kAll, id, 1), least_id = __shfl_sync(kAll, id, K - 1);
+  bool open = lane < K - 1 && ((close >> lane) & 1u) && !alike(id, next_id);
+  int n = K;
+  const bool edge = (close >> (K - 1)) & 1u;
+  if (edge) {
+    n = 0;
+    const float inv_z = fast_rcp(z);
+#pragma unroll 1
+    for (int e0 = 0; e0 < E; e0 += 32) {
+      const int e = min(e0 + lane, E - 1);
+      const float l = clean(logit(row + e));
+      float v = bias ? __fadd_rn(score_of(!softmax, l, top, inv_z), __ldg(bias + e)) : l;
+      bool in = e == e0 + lane && l > kNone && v > kNone && ((kept >> ((e * q.inv_per) >> 20)) & 1u);
+      v = fminf(v, 3.402823466e38f);
+      const float gap = least - v, wide = off + cut * fmaxf(fabsf(least), fabsf(v));
+      in = in && !(gap > wide);
+      if (in && !(-gap > wide) && !alike(e, least_id)) open = true;
+      const unsigned all = __ballot_sync(kAll, in);
+      const int place = n + __popc(all & ((1u << lane) - 1u));
+      if (in && place < 32) list[place] = e;
+      n += __popc(all);
+    }
+  }
+  if (!__any_sync(kAll, open)) return id;
+  if (n > 32) return kTooMany;
+  if (edge) {
+    __syncwarp();
+    id = lane < n ? list[lane] : -1;
+    __syncwarp();  // (read before the next token's are written)
+  }
   double x = id >= 0 ? (double)clean(logit(row + id)) : (double)kNone;
   if (bias) {
-    const int end = softmax ? r.n_experts + r.n_shared : 0;
-    double own = 0.0, z = 0.0;
+    const int end = softmax ? E + r.n_shared : 0;
+    double own = 0.0, sum = 0.0;
 #pragma unroll 1
     for (int e = lane - 32; e < end; e += 32) {  // first the candidate, then the token's sum
       const double l = e < 0 ? x : (double)clean(logit(row + e));
       const double a = exp(softmax ? l - (double)top : -l);
       if (e < 0) own = a;
-      else z += a;
+      else sum += a;
     }
     __syncwarp();
-    z = softmax ? warp_sum(z) : 1.0 + own;
-    x = (softmax ? own : 1.0) / z + (double)__ldg(bias + max(id, 0));
+    sum = softmax ? warp_sum(sum) : 1.0 + own;
+    x = (softmax ? own : 1.0) / sum + (double)__ldg(bias + max(id, 0));
   }
   int before = 0;
   for (int j = 0; j < n; ++j) {
@@ -298,9 +341,14 @@ __device__ __noinline__ int order_fp64(const T *row, const float *bias, const dm
   return mine;
 }
 
+// Registers for a lane's experts: 64 hold 8 of them beside a few spilled values (24,000 tokens of 256
+// experts: 21.3 us, with 72 registers 23.3); 32 want 128 (8,192 tokens of 1,024 experts: 58 us, with 64
+// 78; in 16 groups 63 and 121).
+constexpr int blocks_per_sm(int epl) { return epl >= 32 ? 4 : epl >= 16 ? 6 : 8; }
+
 // kScored: the choice compares scores (a bias, or groups), else the logits themselves.
 template <typename T, int EPL, bool kScored, bool kGroups>
-__global__ void __launch_bounds__(32 * kWarps, 7) route_kernel(const T *__restrict__ logits, int64_t n_tokens,
+__global__ void __launch_bounds__(32 * kWarps, blocks_per_sm(EPL)) route_kernel(const T *__restrict__ logits, int64_t n_tokens,
                                                             const float *__restrict__ bias, const __grid_constant__ Settings q,
                                                             int32_t *__restrict__ ids, float *__restrict__ weights) {
   const dmel_router &r = q.r;
@@ -308,6 +356,8 @@ __global__ void __launch_bounds__(32 * kWarps, 7) route_kernel(const T *__restri
   const int cols = E + S, slots = K + S;
   const unsigned lanes_below = (1u << lane) - 1u;
   const bool sigmoid = r.scoring == DMEL_ROUTE_SIGMOID;
+  constexpr float kCut = cut_of(EPL);
+  __shared__ int list[kWarps][32];  // settle's
   extern __shared__ double smem[];  // with groups: a token's values per warp
   double *const wide = smem + (threadIdx.x >> 5) * q.warp_doubles;
   const int64_t step = (int64_t)gridDim.x * kWarps;
@@ -336,6 +386,7 @@ __global__ void __launch_bounds__(32 * kWarps, 7) route_kernel(const T *__restri
     }
     // what the choice compares, -inf for what is not to be chosen
     bool unsure = false;
+    unsigned kept = ~0u;  // groups
     float v[EPL];
     float off = 0.0f;  // the scores' error
     if (kScored) {
@@ -343,7 +394,7 @@ __global__ void __launch_bounds__(32 * kWarps, 7) route_kernel(const T *__restri
       off = sigmoid ? kSigmoidOff : kSoftmaxOff * inv_z;
 #pragma unroll
       for (int i = 0; i < EPL; ++i) {
-        const float s = sigmoid ? fast_rcp(1.0f + fast_exp(-l[i])) : fast_exp(l[i] - top) * inv_z;
+        const float s = score_of(sigmoid, l[i], top, inv_z);
         v[i] = l[i] > kNone ? s : kNone;
       }
       if (bias) {
@@ -365,8 +416,9 @@ __global__ void __launch_bounds__(32 * kWarps, 7) route_kernel(const T *__restri
       }
       __syncwarp();
       float worst, best;
-      const unsigned kept = keep_groups(narrow, q, &worst, &best);
-      unsure = best > kNone && !(worst - best > margin<1>(2.0f * off, worst, best));  // (two scores a rating)
+      kept = keep_groups(narrow, q, &worst, &best);
+      // two scores a rating
+      unsure = best > kNone && !(worst - best > 4.0f * off + cut_of(1) * fmaxf(fabsf(worst), fabsf(best)));
 #pragma unroll
       for (int i = 0; i < EPL; ++i) {
         const float x = bias ? v[i] : l[i];
@@ -379,68 +431,34 @@ __global__ void __launch_bounds__(32 * kWarps, 7) route_kernel(const T *__restri
     for (int i = 0; i < EPL; ++i) key[i] = key_of<EPL>(v[i], i);
     sort_down<EPL>(key);
     // top_k rounds: the largest head, the lowest lane among equals; slot k's key and lanes stay in lane k
-    float mine = kNone, best = kNone;
-    unsigned holders = 0, heads = 0;
-    auto round = [&](int k) {
-      best = warp_max(key[0]);
+    float mine = kNone;
+    unsigned holders = 1;
+    for (int k = 0; k < K; ++k) {
+      const float best = warp_max(key[0]);
+      if (!(best > kNone)) break;  // nothing left
       const bool held = key[0] == best;
-      heads = __ballot_sync(kAll, held);
+      const unsigned heads = __ballot_sync(kAll, held);
       if (lane == k) {
         mine = best;
         holders = heads;
       }
-      return held && !(heads & lanes_below);
-    };
-    auto drop = [&](bool owner) {
-      if (owner) {
+      if (held && !(heads & lanes_below)) {
 #pragma unroll
         for (int i = 0; i + 1 < EPL; ++i) key[i] = key[i + 1];
         key[EPL - 1] = kNone;
       }
-    };
-    auto expert_of = [&](float k, unsigned lanes) { return __ffs(lanes) - 1 + 32 * place_of<EPL>(k); };
-    const float key_off = bias ? off : 0.0f;
-    auto near = [&](float a, float b) {  // keys a >= b that may stand the other way round in 64 bits
-      const float x = value_of<EPL>(a), y = value_of<EPL>(b);
-      return b > kNone && !(x - y > margin<EPL>(key_off, x, y));
-    };
-    auto alike = [&](int e, int f) { return at(e) == at(f) && (!bias || __ldg(bias + e) == __ldg(bias + f)); };
-    for (int k = 0; k < K; ++k) {
-      const bool owner = round(k);
-      if (!(best > kNone)) break;  // nothing left
-      drop(owner);
     }
-    best = warp_max(key[0]);  // the first that is not chosen
-    int my_id = lane < K && mine > kNone ? expert_of(mine, holders) : -1;  // of slot `lane`
-    const float next = __shfl_down_sync(kAll, mine, 1);
-    const unsigned close = __ballot_sync(kAll, lane < K && near(mine, lane == K - 1 ? best : next));
-    if (close) {
-      // Two experts alike are a tie, which the keys settle by index; with the last of the chosen they
-      // do where no expert that is left is near it and not alike.
-      const bool edge = (close >> (K - 1)) & 1u;
-      const float least = __shfl_sync(kAll, mine, (K - 1) & 31);
-      const int least_id = __shfl_sync(kAll, my_id, (K - 1) & 31), next_id = __shfl_down_sync(kAll, my_id, 1);
-      bool open = lane < K - 1 && ((close >> lane) & 1u) && !alike(my_id, next_id);
-      if (edge) {
-#pragma unroll
-        for (int i = 0; i < EPL; ++i)
-          if (near(least, key[i])) open |= !alike(least_id, lane + 32 * place_of<EPL>(key[i]));
-      }
-      if (__any_sync(kAll, open)) {
-        int n = K;  // the chosen, and all that are near the last of them
-        if (edge) {
-          for (; n < 32; ++n) {
-            const bool owner = round(n);
-            if (!near(least, best)) break;
-            drop(owner);
-          }
-          my_id = lane < n ? expert_of(mine, holders) : -1;
-          if (n == 32) unsure = near(least, warp_max(key[0])) || unsure;
-        }
-        if (!unsure) my_id = order_fp64(row, bias, r, top, my_id, n);
-      }
-    }
-    if (unsure) my_id = choose_fp64<T, EPL>(row, bias, q, top, wide);
+    int my_id = mine > kNone ? __ffs(holders) - 1 + 32 * place_of<EPL>(mine) : -1;  // of slot `lane`
+    // keys that may stand the other way round in 64 bits
+    const float rest = warp_max(key[0]), below = __shfl_down_sync(kAll, mine, 1);
+    const float next = lane == K - 1 ? rest : below, a = value_of<EPL>(mine), b = value_of<EPL>(next);
+    const float wide_off = bias ? 2.0f * off : 0.0f;
+    const bool near = lane < K && next > kNone && !(a - b > wide_off + kCut * fmaxf(fabsf(a), fabsf(b)));
+    const unsigned close = __ballot_sync(kAll, near);
+    if (close)
+      my_id = settle(row, bias, q, top, z, kept, __shfl_sync(kAll, a, K - 1), wide_off, kCut, close, my_id,
+                     list[threadIdx.x >> 5]);
+    if (unsure || my_id == kTooMany) my_id = choose_fp64<T, EPL>(row, bias, q, top, wide);
     float x = lane < K && my_id >= 0 ? at(my_id) : kNone;  // slot `lane`'s logit
     if (lane >= K) my_id = -1;
     if (S > 0) {  // shared experts in slots K .. K + S - 1
@@ -489,8 +507,11 @@ cudaError_t launch_typed(const void *logits, int64_t n_tokens, const float *bias
    : bias                                                                                                           \
        ? route_kernel<T, EPL, true, false><<<grid, 32 * kWarps, 0, stream>>>(lt, n_tokens, bias, q, ids, weights)   \
        : route_kernel<T, EPL, false, false><<<grid, 32 * kWarps, 0, stream>>>(lt, n_tokens, bias, q, ids, weights))
+  // a lane's experts, to the next power of two (8,192 tokens of 384 experts: 21 us, as if 1,024: 49)
   if (E <= 64) DMEL_ROUTE(2);
+  else if (E <= 128) DMEL_ROUTE(4);
   else if (E <= 256) DMEL_ROUTE(8);
+  else if (E <= 512) DMEL_ROUTE(16);
   else DMEL_ROUTE(32);
 #undef DMEL_ROUTE
   return cudaGetLastError();

@@ -168,7 +168,8 @@ def check_route(logits, k, oracle_mod, bias=None, shared=0, sigmoid=True, groups
 @pytest.mark.parametrize("dt", [F32, BF16])
 @pytest.mark.parametrize("sigmoid", [True, False])
 @pytest.mark.parametrize("n,e,shared,k", [(1, 1, 0, 1), (1, 256, 2, 6), (5, 7, 0, 7), (33, 60, 1, 4), (130, 256, 0, 8),
-                                          (64, 31, 3, 5), (64, 33, 0, 2), (17, 1024, 0, 32), (9, 513, 4, 12)])
+                                          (64, 31, 3, 5), (64, 33, 0, 2), (17, 1024, 0, 32), (9, 513, 4, 12), (20, 128, 1, 8), (20, 65, 0, 5),
+                                          (20, 384, 0, 6), (7, 512, 2, 8)])
 def test_route(dt, sigmoid, n, e, shared, k, oracle_mod):
     g = torch.Generator(device=DEV).manual_seed(e + n)
     logits = (2.0 * torch.randn((n, e + shared), generator=g, device=DEV)).to(dt)
