@@ -442,12 +442,13 @@ def dmel_add_rmsnorm(x, rms_weight, out, residual=None, residual_out=None, eps: 
     if len(shape) != 2:
         _refuse(where, f"x: want [rows, dim], got {tuple(shape)}")
     n, d = shape
-    code, odt = _dtype_code(x), out.dtype
+    code, odt = DMEL_BF16 if dt is torch.bfloat16 else _dtype_code(x), out.dtype
     sc = None
     if scales is not None:
         blocks = -(-d // scale_block) if scale_block > 0 else 1
         sc = _addr(scales, where, "scales", torch.float32, (n,) if scales.dim() == 1 and blocks == 1 else (n, blocks), dev)
-    _run_on(dev, stream, where, _lib().dmel_add_rmsnorm, _addr(x, where, "x", dt, shape, dev),
+    _run_on(dev, stream, where, _lib().dmel_add_rmsnorm,
+            x.data_ptr() if x.is_contiguous() else _addr(x, where, "x", dt, shape, dev),
             None if residual is None else _addr(residual, where, "residual", dt, shape, dev), n, d, code,
             _addr(rms_weight, where, "rms_weight", dt, (d,), dev), eps,
             None if residual_out is None else _addr(residual_out, where, "residual_out", dt, shape, dev),
@@ -461,13 +462,17 @@ def dmel_route(logits, ids, weights, n_shared: int = 0, bias=None, scoring: int 
     weights fp32 [T, top_k + n_shared] (their width sets top_k), bias fp32 [n_experts] or None."""
     import torch
     where = "dmel_route"
-    if logits.dim() != 2 or ids.dim() != 2:
-        _refuse(where, f"logits and ids: want two dimensions, got {tuple(logits.shape)} and {tuple(ids.shape)}")
-    dev, n = logits.get_device(), logits.shape[0]
-    e, shape = logits.shape[1] - n_shared, (n, ids.shape[1])
+    all_logits, shape = logits.shape, ids.shape
+    if len(all_logits) != 2 or len(shape) != 2:
+        _refuse(where, f"logits and ids: want two dimensions, got {tuple(all_logits)} and {tuple(shape)}")
+    dt, dev = logits.dtype, logits.get_device()
+    n, e = all_logits[0], all_logits[1] - n_shared
+    shape = (n, shape[1])
     r = _router(e, n_shared, shape[1] - n_shared, n_groups, topk_groups, scoring, int(renormalise), scale)
-    _run_on(dev, stream, where, _lib().dmel_route, _addr(logits, where, "logits", logits.dtype, logits.shape, dev), n,
-            _dtype_code(logits), None if bias is None else _addr(bias, where, "bias", torch.float32, (e,), dev), r,
+    _run_on(dev, stream, where, _lib().dmel_route,
+            logits.data_ptr() if logits.is_contiguous() else _addr(logits, where, "logits", dt, all_logits, dev), n,
+            DMEL_F32 if dt is torch.float32 else _dtype_code(logits),
+            None if bias is None else _addr(bias, where, "bias", torch.float32, (e,), dev), r,
             _addr(ids, where, "ids", torch.int32, shape, dev), _addr(weights, where, "weights", torch.float32, shape, dev))
 
 
