@@ -20,6 +20,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
+#include <math_constants.h>
 #include <stdint.h>
 
 #include "common.cuh"
@@ -41,8 +42,8 @@ struct TokenTile {
 // The slots in expert order, stable, by counting: a warp counts its chunk of slots per expert, a
 // scan over (expert, block, warp) turns the counts into row numbers, and the same walk hands them
 // out. Bound by the matching of 32 slots at a time (about 190 cycles of a scheduler each): one
-// block for few slots, else a cluster of eight that read each other's counts (24,576 slots:
-// 38 us with one block).
+// block for few slots, else a cluster of eight that read each other's counts (24,576 slots: 11 us,
+// with one block 38).
 constexpr int kPlanThreads = 1024;
 constexpr int kAhead = 8;  // slots per lane whose ids are loaded before any is counted
 
@@ -199,7 +200,8 @@ __global__ void __launch_bounds__(kPlanThreads) experts_plan_kernel(const Shared
 // memory, by comparing each slot with all others. The `writer` block also leaves it in memory for
 // the second product, and clears its counters. With the sums in the second product that saves two
 // launches: one token's 6 slots 49.5 us against 53. With 384 slots both cost more than the launches
-// (277 us against 208: the comparisons, and a fence per tile).
+// (277 us against 208: the comparisons, and a fence per tile; a plan by counting in every block, 31 us
+// against 29 for 128 slots of 2048 x 512).
 constexpr int kSmallSlots = 64;
 
 struct SmallPlan {
@@ -271,7 +273,7 @@ __device__ __forceinline__ void make_small_plan(const Shared &c, int tile_tokens
 // the gate's columns and the 64 up columns beside them, the epilogue writes bf16(silu(g) u) to
 // h [rows x hidden]. Otherwise: 128 columns of the down product per CTA, written as a slot's row in
 // fp16 with a power-of-two scale per 128 columns, or in fp32 in a small call. (fp32 rows, written
-// and read back, cost a prompt of 4,096 tokens 937 us against 887. 11 bits beside the scale are off
+// and read back, cost a prompt of 4,096 tokens 50 us of 937. 11 bits beside the scale are off
 // by 2^-11 at most, an eighth of the rounding of the gated row and of the output to bf16; the
 // tokens' sums are fp32.)
 template <int kTokens, bool kSmall = false, bool kTall = false>
@@ -341,10 +343,14 @@ __device__ __forceinline__ float warp_max(float v) {
 
 // The power of two that takes a block's largest magnitude to [2^14, 2^15), inside fp16's range with
 // 28 binades of normal numbers below. Between 2^-112 and 2^112, so that it and its reciprocal are
-// normal fp32 numbers; 1 for an infinity, which stays one.
-__device__ __forceinline__ float row_scale_up(float top) {
-  const int e = (int)(__float_as_uint(top) >> 23);  // biased exponent; 255: infinity
-  const int up = e == 255 ? 127 : 127 + 14 + 127 - e;
+// normal fp32 numbers. A warp's lanes hold the block; what is not finite does not enter and stays so.
+__device__ __forceinline__ float row_scale_up(float4 r) {
+  float top = warp_max(fmaxf(fmaxf(fabsf(r.x), fabsf(r.y)), fmaxf(fabsf(r.z), fabsf(r.w))));
+  if (!(top < CUDART_INF_F)) {
+    auto finite = [](float v) { return fabsf(v) < CUDART_INF_F ? fabsf(v) : 0.0f; };
+    top = warp_max(fmaxf(fmaxf(finite(r.x), finite(r.y)), fmaxf(finite(r.z), finite(r.w))));
+  }
+  const int up = 127 + 14 + 127 - (int)(__float_as_uint(top) >> 23);  // (of the biased exponent)
   return __uint_as_float((uint32_t)min(max(up, 127 - 112), 127 + 112) << 23);
 }
 
@@ -694,9 +700,7 @@ __global__ void __launch_bounds__(kGate ? EX<kTokens, kSmall, kTall>::THREADS_GA
             float up[8];
             // (columns past the last are zeros: the weights' fill)
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-              up[j] = row_scale_up(
-                  warp_max(fmaxf(fmaxf(fabsf(r[j].x), fabsf(r[j].y)), fmaxf(fabsf(r[j].z), fabsf(r[j].w)))));
+            for (int j = 0; j < 8; ++j) up[j] = row_scale_up(r[j]);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
               const int k = k0 + 4 * j;

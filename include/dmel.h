@@ -415,9 +415,9 @@ dmel_status dmel_route(const void *logits, int64_t n_tokens, dmel_dtype dtype, c
  * workspace device scratch of dmel_experts_workspace_size(...) bytes, 256-byte aligned; calls that
  *           may run at the same time need one each
  * Products sum in fp32; the gated hidden row is rounded to bf16 once (the second product's
- * operand), each expert's output row to 11 bits beside a scale per 128 columns, and the token's
- * fp32 sum to bf16.
- * Results do not depend on how tokens are batched, up to fp32 summation inside the tensor cores.
+ * operand), with more than 64 slots each expert's output row to 11 bits beside a scale per 128
+ * columns, and the token's fp32 sum to bf16. How tokens are batched changes no more than that
+ * rounding and the order of fp32 sums.
  * n_tokens * slots at most 2^30. Asynchronous on stream; two to four launches, by the number of slots. */
 typedef struct {
   int n_experts;     /* 1 .. 1024 */

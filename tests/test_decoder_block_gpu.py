@@ -478,6 +478,23 @@ def test_experts_nan_stays_with_its_token():
     assert torch.equal(out[rest], clean[rest])
 
 
+def test_experts_infinity_stays_in_its_column():
+    """Columns whose products overflow, beside columns far above fp16's range and far below it."""
+    x, ids, w, w_in, w_out = expert_inputs(64, 90, 2, 3, 200, 72)
+    x = x.abs() + 1.0
+    w_in[:, :, 0] = w_in[:, :, 72] = 1e8  # gate and up sums of 2e10 and more: a hidden value above 4e20 ...
+    w_out[:, 0] = 0.0                     # ... which no column reads
+    w_out[:, :, 20:40] *= 1e7
+    w_out[:, :, 130:150] *= 1e-7
+    clean = run_experts(x, ids, w, w_in, w_out)
+    assert clean.isfinite().all()
+    w_out[:, 0, 5] = w_out[:, 0, 140] = 1e30  # two that do
+    out = run_experts(x, ids, w, w_in, w_out)
+    assert not out[:, [5, 140]].isfinite().any()
+    others = [c for c in range(200) if c not in (5, 140)]
+    assert torch.equal(out[:, others], clean[:, others])
+
+
 def test_experts_same_bits_every_time_and_rows_behind():
     x, ids, w, w_in, w_out = expert_inputs(63, 600, 4, 7, 264, 136)
     first = run_experts(x, ids, w, w_in, w_out)
