@@ -117,7 +117,7 @@ struct Scales {
 // takes the block (and its address is the same in every thread, which saves registers).
 // Two pieces and 32 registers: what bounds the rate is how many threads an SM holds (2,048) and
 // then, for e4m3, the instructions per value. 24,000 x 6144 bf16 with the stream in and out: 183 us,
-// 6.4 TB/s (64 registers 198 us, one piece 230 us); 12,800 rows into e4m3 by 128 columns: 99 us.
+// 6.4 TB/s (64 registers 198 us, one piece 230 us); 12,800 rows into e4m3 by 128 columns: 100 us.
 // With no more rows than SMs one piece is the shorter way (8 rows: 2.4 us against 3.0), and for fp32
 // rows, which have twice the bytes per piece, it is the faster one (1,601 x 5992: 25 us against 29).
 template <typename T, typename TO, int V, bool kWarpRows>
@@ -171,7 +171,15 @@ __global__ void __launch_bounds__(1024, 2) add_rmsnorm_kernel(const T *x, const 
       }
     }
     ss = block_reduce(ss, red[turn][0], warps, Add());
-    const float rstd = rsqrtf(fmaf(ss, inv_dim, eps));  // (within 2 ulps, on the special-function unit)
+    float rstd = rsqrtf(fmaf(ss, inv_dim, eps));  // (within 2 ulps, on the special-function unit)
+    if (sizeof(TO) == 1 && rstd > 1e4f) {  // rstd / scale would leave fp32's range: rstd first
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s[j][i] *= rstd;
+      }
+      rstd = 1.0f;
+    }
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       const uint32_t p = j * blockDim.x + threadIdx.x;

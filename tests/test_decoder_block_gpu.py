@@ -109,6 +109,26 @@ def test_add_rmsnorm_zero_rows_nan_and_infinity():
     torch.testing.assert_close(out[4], 1e-30 / 1e-3 * w, rtol=1e-5, atol=0)
 
 
+@pytest.mark.parametrize("eps", [1e-12, 1e-30])
+@pytest.mark.parametrize("block", [0, 32, 128])
+def test_add_rmsnorm_e4m3_rows_next_to_zero(block, eps, oracle_mod):
+    """Padding rows and rows of 1e-36 with a small eps: 1 / sqrt(eps) / scale is above fp32's range."""
+    d = 264
+    x, _, w = norm_inputs(4, 4, d, F32, residual=False)
+    x[1] = 0.0
+    x[2] *= 1e-36
+    blocks = -(-d // block) if block else 1
+    out, sc = torch.empty((4, d), dtype=E4M3, device=DEV), torch.empty((4, blocks), device=DEV)
+    dmel.dmel_add_rmsnorm(x, w, out, eps=eps, scales=sc, scale_block=block)
+    _, y, ref = oracle_mod.add_rmsnorm(f64(x), None, f64(w), float(np.float32(eps)), block)
+    b = norm_bound(d) + 4 * 2.0 ** -24
+    assert (np.abs(f64(sc) - ref) <= b * ref).all()
+    q, each = f64(out.float()), np.repeat(ref, block or d, axis=1)[:, :d]
+    # w s itself (1e-36) is rounded to fp32's normal numbers
+    assert (np.abs(q - y / each) <= (2.0 ** -4 + 2 * b) * np.abs(y / each) + 2.0 ** -10).all()
+    assert (q[1] == 0).all()
+
+
 @pytest.mark.parametrize("dt", [F32, BF16])
 def test_add_rmsnorm_in_place(dt):
     """The stream updated in its own buffer and the normed rows over x: the same bits; rows behind the
