@@ -199,7 +199,7 @@ __global__ void __launch_bounds__(kPlanThreads) experts_plan_kernel(const Shared
 // The same for at most kSmallSlots slots, by every block of the first product for itself in shared
 // memory, by comparing each slot with all others. The `writer` block also leaves it in memory for
 // the second product, and clears its counters. With the sums in the second product that saves two
-// launches: one token's 6 slots 49.5 us against 53. With 384 slots both cost more than the launches
+// launches: one token's 6 slots 49.2 us against 53. With 384 slots both cost more than the launches
 // (277 us against 208: the comparisons, and a fence per tile; a plan by counting in every block, 31 us
 // against 29 for 128 slots of 2048 x 512).
 constexpr int kSmallSlots = 64;
@@ -363,8 +363,9 @@ __device__ __forceinline__ float4 row4(const uint2 u, float scale) {
 
 // Called by the 256 epilogue threads after their writes of a work item: whether this is the last of n
 // items to come here (whatever the order), whose threads then see the others' writes. Nothing waits.
+// (One thread's fences after the barrier cover the others' writes; a fence in each costs a
+// microsecond more per call.)
 __device__ __forceinline__ bool last_of(int n, int *counter, int *flag) {
-  __threadfence();
   asm volatile("bar.sync 3, 256;" ::: "memory");
   if (threadIdx.x == 64) {
     __threadfence();
@@ -397,18 +398,32 @@ __device__ __forceinline__ void join_splits(const Shared &c, __nv_bfloat16 *h, i
   }
 }
 
+// The slots' rows and weights in shared memory, for small_sum: read by the 256 epilogue threads while
+// the products run.
+struct SmallSlots {
+  int row[kSmallSlots];
+  float weight[kSmallSlots];
+};
+__device__ __forceinline__ void load_slots(const Shared &c, SmallSlots *s) {
+  const int i = threadIdx.x - 64;
+  if (i >= c.n_slots) return;
+  const int r = c.plan.row[i];
+  s->row[i] = r;
+  s->weight[i] = r < 0 ? 0.0f : c.weights[i];
+}
+
 // 128 columns from `col` on of every token's weighted sum, by the 256 epilogue threads: the rows y
 // (dim columns each, other blocks' work among them) in slot order.
-__device__ __forceinline__ void small_sum(const Shared &c, const float *y, int dim, int col) {
+__device__ __forceinline__ void small_sum(const Shared &c, const SmallSlots &s, const float *y, int dim, int col) {
   const int et = threadIdx.x - 64, q = col + 4 * (et & 31), n_tokens = c.n_slots / c.slots;
   if (q >= dim) return;
   for (int t = et >> 5; t < n_tokens; t += 8) {
     float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 4
     for (int j = 0; j < c.slots; ++j) {
-      const int r = __ldcg(c.plan.row + t * c.slots + j);
+      const int r = s.row[t * c.slots + j];
       if (r < 0) continue;
-      const float w = c.weights[t * c.slots + j];
+      const float w = s.weight[t * c.slots + j];
       const float4 v = __ldcg(reinterpret_cast<const float4 *>(y + (int64_t)r * dim + q));
       acc.x = fmaf(w, v.x, acc.x);
       acc.y = fmaf(w, v.y, acc.y);
@@ -497,6 +512,14 @@ __global__ void __launch_bounds__(kGate ? EX<kTokens, kSmall, kTall>::THREADS_GA
   auto tile_of = [&](int64_t u) { return kSplit ? u / splits : u; };
   auto token_tile = [&](int64_t u) { return tiles[tile_of(u) / n_ct]; };
   auto column = [&](int64_t u) { return (int)(tile_of(u) % n_ct) * 2 * COLS + (int)rank * COLS; };
+  // The rows of a tile that CTA r loads: those of its half that are there, to a whole load of 4 (gathered)
+  // or 8. What lies behind them in shared memory is multiplied into columns that nobody stores. (One
+  // token's 6 experts: 49.2 us, with the token's row gathered into all 16 places 55.)
+  constexpr int LOAD = kGate ? 4 : 8;
+  auto rows_of = [&](const TokenTile &tt, int r) {
+    const int half = tt.width / 2, left = tt.rows - r * half;
+    return (min(max(left, 0), half) + LOAD - 1) / LOAD * LOAD;
+  };
   auto kb_begin = [&](int64_t u) { return kSplit ? KB * (int)(u % splits) / splits : 0; };
   auto kb_end = [&](int64_t u) { return kSplit ? KB * ((int)(u % splits) + 1) / splits : KB; };
 
@@ -508,8 +531,8 @@ __global__ void __launch_bounds__(kGate ? EX<kTokens, kSmall, kTall>::THREADS_GA
     for (int64_t t = blockIdx.x >> 1; ok && t < total; t += step) {
       const TokenTile tt = token_tile(t);
       const int col = column(t), kb1 = kb_end(t);
-      const int half = tt.width / 2;  // token rows of this CTA, a multiple of 8
-      const uint32_t bytes = 2u * (X::A_STAGE + (uint32_t)half * 128u);
+      const int rows = rows_of(tt, (int)rank);
+      const uint32_t bytes = 2u * X::A_STAGE + 128u * (uint32_t)(rows_of(tt, 0) + rows_of(tt, 1));
       for (int kb = kb_begin(t); kb < kb1; ++kb) {
         if (!__all_sync(kAll, mbar_wait(empty(stage), phase ^ 1u, err))) { ok = false; break; }
         if (elect_one()) {
@@ -524,12 +547,12 @@ __global__ void __launch_bounds__(kGate ? EX<kTokens, kSmall, kTall>::THREADS_GA
             tma_load_3d_pair(a_dst + (2 * set + 1) * X::BOX, &wmap, c0 + (kGate ? cols : 64), kb * BK, tt.expert, fb);
           }
           if (!kGate) {
-            // rows past the tile are the next expert's, or zeros past the last: computed, not stored
+            // rows past the tile in its last box are the next expert's, or zeros past the last
             const uint32_t b_dst = smem_addr(smem + X::OFF_B + stage * X::B_STAGE);
-            const int row = tt.row0 + (int)rank * half;
+            const int row = tt.row0 + (int)rank * (tt.width / 2);
             int r = 0;
-            for (; r + 32 <= half; r += 32) tma_load_2d_pair(b_dst + r * 128, &xmap, kb * BK, row + r, fb);
-            for (; r < half; r += 8) tma_load_2d_pair(b_dst + r * 128, &xmap8, kb * BK, row + r, fb);
+            for (; r + 32 <= rows; r += 32) tma_load_2d_pair(b_dst + r * 128, &xmap, kb * BK, row + r, fb);
+            for (; r < rows; r += 8) tma_load_2d_pair(b_dst + r * 128, &xmap8, kb * BK, row + r, fb);
           }
         }
         __syncwarp();
@@ -595,7 +618,7 @@ __global__ void __launch_bounds__(kGate ? EX<kTokens, kSmall, kTall>::THREADS_GA
     bool ok = true;
     for (int64_t t = blockIdx.x >> 1; ok && t < total; t += step) {
       const TokenTile tt = token_tile(t);
-      const int kb1 = kb_end(t), groups = tt.width / 8;  // of four rows, in this CTA's half
+      const int kb1 = kb_end(t), groups = rows_of(tt, (int)rank) / 4;
       __syncwarp();                     // the last tile's numbers have been read
       for (int g = w + X::GATHER_WARPS * lane; g < groups; g += X::GATHER_WARPS * 32) {
         int r[4];
@@ -629,6 +652,9 @@ __global__ void __launch_bounds__(kGate ? EX<kTokens, kSmall, kTall>::THREADS_GA
     const int quad = warp & 3, group = (warp - 2) >> 2, et = (threadIdx.x - 64) & 127;
     float *const buf = reinterpret_cast<float *>(smem + X::OFF_STG + group * X::STG);
     int *last = reinterpret_cast<int *>(smem + X::OFF_LAST);
+    SmallSlots *const slots = reinterpret_cast<SmallSlots *>(smem + X::OFF_PLAN);  // (last_of's barrier is between)
+    static_assert(sizeof(SmallSlots) <= sizeof(SmallPlan), "shared memory of the small plan");
+    if (kSmall && !kGate) load_slots(shared, slots);
     uint32_t i = 0;
     bool ok = true;
     for (int64_t t = blockIdx.x >> 1; t < total; t += step, ++i) {
@@ -727,12 +753,14 @@ __global__ void __launch_bounds__(kGate ? EX<kTokens, kSmall, kTall>::THREADS_GA
       if (kSmall && !kGate) {
         // these columns of all tokens, when every token tile has been through them
         if (last_of(token_tiles, shared.counters + 2 * (t % n_ct) + rank, last))
-          small_sum(shared, static_cast<const float *>(out), cols, first_col);
+          small_sum(shared, *slots, static_cast<const float *>(out), cols, first_col);
       }
     }
-    if (kSmall && !kGate && token_tiles == 0)  // no token has an expert: zeros
+    if (kSmall && !kGate && token_tiles == 0) {  // no token has an expert: zeros
+      asm volatile("bar.sync 3, 256;" ::: "memory");
       for (int64_t ct = blockIdx.x >> 1; ct < n_ct; ct += step)
-        small_sum(shared, static_cast<const float *>(out), cols, (int)ct * 2 * COLS + (int)rank * COLS);
+        small_sum(shared, *slots, static_cast<const float *>(out), cols, (int)ct * 2 * COLS + (int)rank * COLS);
+    }
   }
 
   tc_fence_before();
