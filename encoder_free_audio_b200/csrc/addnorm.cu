@@ -45,13 +45,15 @@ __device__ __forceinline__ void load8(const __nv_bfloat16 *p, float (&v)[8]) {
                : "memory");
   unpack8(u, v);
 }
+// (Plain loads: what a launch reads may be written until wait_for_predecessors, above which the
+// compiler may take loads of read-only memory.)
 __device__ __forceinline__ void weight8(const float *p, float (&v)[8]) {
-  const float4 a = __ldg(reinterpret_cast<const float4 *>(p)), b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
+  const float4 a = *reinterpret_cast<const float4 *>(p), b = *(reinterpret_cast<const float4 *>(p) + 1);
   v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
   v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
 }
 __device__ __forceinline__ void weight8(const __nv_bfloat16 *p, float (&v)[8]) {
-  const uint4 q = __ldg(reinterpret_cast<const uint4 *>(p));
+  const uint4 q = *reinterpret_cast<const uint4 *>(p);
   const uint32_t u[4] = {q.x, q.y, q.z, q.w};
   unpack8(u, v);
 }
@@ -122,9 +124,11 @@ struct Scales {
 // rows, which have twice the bytes per piece, it is the faster one (1,601 x 5992: 25 us against 29).
 template <typename T, typename TO, int V, bool kWarpRows>
 __global__ void __launch_bounds__(1024, 2) add_rmsnorm_kernel(const T *x, const T *res, int64_t n_rows, int dim,
-                                                              const T *__restrict__ w, float eps, T *res_out, TO *out,
+                                                              const T *w, float eps, T *res_out, TO *out,
                                                               Scales sc) {
   __shared__ float red[2][2][32];
+  wait_for_predecessors();
+  launch_dependents();
   const int warps = kWarpRows ? 1 : blockDim.x >> 5, pieces = dim >> 3;
   const float inv_dim = 1.0f / (float)dim;
   const int64_t step = (int64_t)gridDim.x * (kWarpRows ? blockDim.y : 1);
@@ -273,14 +277,15 @@ cudaError_t launch_typed(const void *x, const void *res, int64_t n_rows, int dim
   const T *xt = static_cast<const T *>(x), *rt = static_cast<const T *>(res), *wt = static_cast<const T *>(w);
   T *so = static_cast<T *>(res_out);
   TO *ot = static_cast<TO *>(out);
+  cudaLaunchAttribute at;
+  const cudaLaunchConfig_t cfg = programmatic_launch(grid, block, 0, stream, &at);
 #define DMEL_NORM(V, ROWS) \
-  add_rmsnorm_kernel<T, TO, V, ROWS><<<grid, block, 0, stream>>>(xt, rt, n_rows, dim, wt, eps, so, ot, sc)
+  return cudaLaunchKernelEx(&cfg, add_rmsnorm_kernel<T, TO, V, ROWS>, xt, rt, n_rows, dim, wt, eps, so, ot, sc)
   if (warp_rows && two) DMEL_NORM(2, true);
   else if (warp_rows) DMEL_NORM(1, true);
   else if (two) DMEL_NORM(2, false);
   else DMEL_NORM(1, false);
 #undef DMEL_NORM
-  return cudaGetLastError();
 }
 
 }  // namespace

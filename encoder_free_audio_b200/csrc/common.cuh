@@ -197,9 +197,27 @@ __device__ __forceinline__ bool elect_one() {
 }
 
 // Programmatic dependent launch: the next kernel of the stream (launched with that attribute) may
-// start; wait until the kernels before this one have finished and their writes are seen.
+// start; wait until the kernels before this one have finished and their writes are seen. A kernel
+// waits before it touches memory and only then lets the next one start, so of a stream's kernels none
+// starts before all but its predecessor are done. What a launch costs then lies under the end of the
+// kernel before (per call: dmel_add_rmsnorm 2 us, dmel_route 0.5 to 1, dmel_experts 1.5 to 3).
 __device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void wait_for_predecessors() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// A launch with that attribute, which the caller's *at holds.
+inline cudaLaunchConfig_t programmatic_launch(dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
+                                              cudaLaunchAttribute *at) {
+  at->id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at->val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cfg;
+}
 
 // ---------------------------------------------------------------- clusters of two CTAs (cta_group::2)
 

@@ -78,9 +78,10 @@ __global__ void __launch_bounds__(kPlanThreads) experts_plan_kernel(const Shared
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int *total = hist + 32 * E, *first = total + E;
   const unsigned block = cluster_ctarank(), blocks = gridDim.x;  // one cluster
+  wait_for_predecessors();
+  launch_dependents();
   if (block == 0)
     for (int i = threadIdx.x; i < call.n_counters; i += kPlanThreads) call.counters[i] = 0;
-  launch_dependents();
   // slots per warp, a multiple of 32 (n_slots <= 2^30)
   const int walkers = 32 * (int)blocks, chunk = ((n_slots + walkers - 1) / walkers + 31) / 32 * 32;
   const int walker = (int)block * 32 + warp;
@@ -199,7 +200,7 @@ __global__ void __launch_bounds__(kPlanThreads) experts_plan_kernel(const Shared
 // The same for at most kSmallSlots slots, by every block of the first product for itself in shared
 // memory, by comparing each slot with all others. The `writer` block also leaves it in memory for
 // the second product, and clears its counters. With the sums in the second product that saves two
-// launches: one token's 6 slots 49.2 us against 53. With 384 slots both cost more than the launches
+// launches: one token's 6 slots 49.5 us against 53 (before what came later to both). With 384 slots both cost more than the launches
 // (277 us against 208: the comparisons, and a fence per tile; a plan by counting in every block, 31 us
 // against 29 for 128 slots of 2048 x 512).
 constexpr int kSmallSlots = 64;
@@ -444,7 +445,7 @@ __device__ __forceinline__ void small_sum(const Shared &c, const SmallSlots &s, 
 template <int kTokens, bool kGate, bool kSmall, bool kSplit, bool kTall>
 __global__ void __launch_bounds__(kGate ? EX<kTokens, kSmall, kTall>::THREADS_GATE : EX<kTokens, kSmall, kTall>::THREADS, 1)
     experts_product_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
-                           const __grid_constant__ CUtensorMap xmap8, const int *__restrict__ n_tiles,
+                           const __grid_constant__ CUtensorMap xmap8, const int *n_tiles,
                            const TokenTile *tiles, const int *token, int K, int cols, void *out, const Shared shared,
                            uint32_t *err) {
   using X = EX<kTokens, kSmall, kTall>;
@@ -774,11 +775,11 @@ __global__ void __launch_bounds__(kGate ? EX<kTokens, kSmall, kTall>::THREADS_GA
 // ---------------------------------------------------------------- the tokens' weighted sums
 //
 // Reads each chosen slot's row once: HBM bound (or L2, where the rows still lie there).
-__global__ void __launch_bounds__(256) experts_sum_kernel(const __half *__restrict__ y, const float *__restrict__ scales,
-                                                          const int *__restrict__ row, const float *__restrict__ weights,
-                                                          int64_t n_tokens, int slots, int dim,
-                                                          __nv_bfloat16 *__restrict__ out) {
+__global__ void __launch_bounds__(256) experts_sum_kernel(const __half *y, const float *scales, const int *row,
+                                                          const float *weights, int64_t n_tokens, int slots, int dim,
+                                                          __nv_bfloat16 *out) {
   wait_for_predecessors();
+  launch_dependents();
   const int pieces = dim / 8, n_blocks = (dim + 127) / 128;
   const int64_t total = n_tokens * pieces;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
@@ -923,7 +924,7 @@ cudaError_t launch_product(const Call &c) {
   at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
-  cfg.numAttrs = kSmall && kGate ? 1 : 2;  // (the first launch of a call starts when all before it is done)
+  cfg.numAttrs = 2;
   const PlanOut &p = c.shared.plan;
   return cudaLaunchKernelEx(&cfg, kernel, kGate ? c.in_w : c.out_w, kGate ? c.in_x : c.out_h, c.out_h8,
                             (const int *)p.n_tiles, (const TokenTile *)p.tiles, (const int *)p.token,
@@ -959,13 +960,15 @@ cudaError_t launch_plan(const Call &c, int tile_tokens, int *launches) {
   cfg.blockDim = dim3(kPlanThreads);
   cfg.dynamicSmemBytes = (size_t)34 * s.n_experts * 4;
   cfg.stream = c.stream;
-  cudaLaunchAttribute at[1];
+  cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeClusterDimension;
   at[0].val.clusterDim.x = blocks;
   at[0].val.clusterDim.y = 1;
   at[0].val.clusterDim.z = 1;
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   e = cudaLaunchKernelEx(&cfg, experts_plan_kernel, s, tile_tokens, c.err);
   if (e == cudaSuccess) ++*launches;
   return e;
@@ -973,15 +976,8 @@ cudaError_t launch_plan(const Call &c, int tile_tokens, int *launches) {
 
 cudaError_t launch_sum(const Call &c, int64_t n_tokens, int *launches) {
   const int64_t blocks = (n_tokens * (c.dim / 8) + 255) / 256, cap = (int64_t)c.num_sms * 32;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(blocks < cap ? blocks : cap));
-  cfg.blockDim = dim3(256);
-  cfg.stream = c.stream;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
+  cudaLaunchAttribute at;
+  const cudaLaunchConfig_t cfg = programmatic_launch(dim3((unsigned)(blocks < cap ? blocks : cap)), dim3(256), 0, c.stream, &at);
   const cudaError_t e = cudaLaunchKernelEx(&cfg, experts_sum_kernel, (const __half *)c.y, (const float *)c.shared.scales, (const int *)c.shared.plan.row,
                                            c.shared.weights, n_tokens, c.shared.slots, c.dim, c.shared.out);
   if (e == cudaSuccess) ++*launches;

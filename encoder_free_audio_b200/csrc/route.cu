@@ -31,7 +31,9 @@ constexpr int kWarps = 4;  // per block
 constexpr unsigned kAll = 0xffffffffu;
 constexpr float kNone = -__builtin_huge_valf();  // "not to be chosen"
 
-__device__ __forceinline__ float logit(const float *p) { return __ldg(p); }
+// (Plain loads: what a launch reads may be written until wait_for_predecessors, above which the
+// compiler may take loads of read-only memory.)
+__device__ __forceinline__ float logit(const float *p) { return *p; }
 __device__ __forceinline__ float logit(const __nv_bfloat16 *p) { return __bfloat162float(*p); }
 
 // A logit as the choice sees it: NaN is -inf (never chosen; fmaxf drops it), +inf the largest finite
@@ -215,7 +217,7 @@ __device__ __noinline__ int choose_fp64(const T *row, const float *bias, const S
     for (int i = 0; i < EPL; ++i) {
       const int e = lane + 32 * i;
       double x = softmax ? c[i] * z : c[i];
-      if (bias && e < E) x += (double)__ldg(bias + e);
+      if (bias && e < E) x += (double)bias[e];
       c[i] = e < E && clean(logit(row + e)) > kNone && x == x ? x : (double)kNone;
     }
   }
@@ -280,7 +282,7 @@ __device__ __noinline__ int settle(const T *row, const float *bias, const Settin
   const int lane = threadIdx.x & 31, E = r.n_experts, K = r.top_k;
   const bool softmax = r.scoring == DMEL_ROUTE_SOFTMAX;
   auto alike = [&](int e, int f) {
-    return clean(logit(row + e)) == clean(logit(row + f)) && (!bias || __ldg(bias + e) == __ldg(bias + f));
+    return clean(logit(row + e)) == clean(logit(row + f)) && (!bias || bias[e] == bias[f]);
   };
   const int next_id = __shfl_down_sync(kAll, id, 1), least_id = __shfl_sync(kAll, id, K - 1);
   bool open = lane < K - 1 && ((close >> lane) & 1u) && !alike(id, next_id);
@@ -293,7 +295,7 @@ __device__ __noinline__ int settle(const T *row, const float *bias, const Settin
     for (int e0 = 0; e0 < E; e0 += 32) {
       const int e = min(e0 + lane, E - 1);
       const float l = clean(logit(row + e));
-      float v = bias ? __fadd_rn(score_of(!softmax, l, top, inv_z), __ldg(bias + e)) : l;
+      float v = bias ? __fadd_rn(score_of(!softmax, l, top, inv_z), bias[e]) : l;
       bool in = e == e0 + lane && l > kNone && v > kNone && ((kept >> ((e * q.inv_per) >> 20)) & 1u);
       v = fminf(v, 3.402823466e38f);
       const float gap = least - v, wide = off + cut * fmaxf(fabsf(least), fabsf(v));
@@ -325,7 +327,7 @@ __device__ __noinline__ int settle(const T *row, const float *bias, const Settin
     }
     __syncwarp();
     sum = softmax ? warp_sum(sum) : 1.0 + own;
-    x = (softmax ? own : 1.0) / sum + (double)__ldg(bias + max(id, 0));
+    x = (softmax ? own : 1.0) / sum + (double)bias[max(id, 0)];
   }
   int before = 0;
   for (int j = 0; j < n; ++j) {
@@ -348,9 +350,11 @@ constexpr int blocks_per_sm(int epl) { return epl >= 32 ? 4 : epl >= 16 ? 6 : 8;
 
 // kScored: the choice compares scores (a bias, or groups), else the logits themselves.
 template <typename T, int EPL, bool kScored, bool kGroups>
-__global__ void __launch_bounds__(32 * kWarps, blocks_per_sm(EPL)) route_kernel(const T *__restrict__ logits, int64_t n_tokens,
-                                                            const float *__restrict__ bias, const __grid_constant__ Settings q,
-                                                            int32_t *__restrict__ ids, float *__restrict__ weights) {
+__global__ void __launch_bounds__(32 * kWarps, blocks_per_sm(EPL)) route_kernel(const T *logits, int64_t n_tokens,
+                                                            const float *bias, const __grid_constant__ Settings q,
+                                                            int32_t *ids, float *weights) {
+  wait_for_predecessors();
+  launch_dependents();
   const dmel_router &r = q.r;
   const int lane = threadIdx.x & 31, E = r.n_experts, S = r.n_shared, K = r.top_k;
   const int cols = E + S, slots = K + S;
@@ -400,7 +404,7 @@ __global__ void __launch_bounds__(32 * kWarps, blocks_per_sm(EPL)) route_kernel(
       if (bias) {
 #pragma unroll
         for (int i = 0; i < EPL; ++i)
-          if (lane + 32 * i < E) v[i] += __ldg(bias + lane + 32 * i);
+          if (lane + 32 * i < E) v[i] += bias[lane + 32 * i];
       }
     } else {
 #pragma unroll
@@ -501,12 +505,15 @@ cudaError_t launch_typed(const void *logits, int64_t n_tokens, const float *bias
   const size_t smem = (size_t)kWarps * q.warp_doubles * sizeof(double);
   const int64_t blocks = (n_tokens + kWarps - 1) / kWarps, cap = (int64_t)num_sms * 64;
   const unsigned grid = (unsigned)(blocks < cap ? blocks : cap);
-#define DMEL_ROUTE(EPL)                                                                                             \
-  (r.n_groups > 1                                                                                                   \
-       ? route_kernel<T, EPL, true, true><<<grid, 32 * kWarps, smem, stream>>>(lt, n_tokens, bias, q, ids, weights) \
-   : bias                                                                                                           \
-       ? route_kernel<T, EPL, true, false><<<grid, 32 * kWarps, 0, stream>>>(lt, n_tokens, bias, q, ids, weights)   \
-       : route_kernel<T, EPL, false, false><<<grid, 32 * kWarps, 0, stream>>>(lt, n_tokens, bias, q, ids, weights))
+  cudaLaunchAttribute at;
+  const cudaLaunchConfig_t cfg = programmatic_launch(grid, dim3(32 * kWarps), smem, stream, &at);
+#define DMEL_ROUTE(EPL)                                                                                      \
+  return r.n_groups > 1 ? cudaLaunchKernelEx(&cfg, route_kernel<T, EPL, true, true>, lt, n_tokens, bias, q,   \
+                                             ids, weights)                                                    \
+         : bias         ? cudaLaunchKernelEx(&cfg, route_kernel<T, EPL, true, false>, lt, n_tokens, bias, q,  \
+                                             ids, weights)                                                    \
+                        : cudaLaunchKernelEx(&cfg, route_kernel<T, EPL, false, false>, lt, n_tokens, bias, q, \
+                                             ids, weights)
   // a lane's experts, to the next power of two (8,192 tokens of 384 experts: 21 us, as if 1,024: 49)
   if (E <= 64) DMEL_ROUTE(2);
   else if (E <= 128) DMEL_ROUTE(4);
@@ -514,7 +521,6 @@ cudaError_t launch_typed(const void *logits, int64_t n_tokens, const float *bias
   else if (E <= 512) DMEL_ROUTE(16);
   else DMEL_ROUTE(32);
 #undef DMEL_ROUTE
-  return cudaGetLastError();
 }
 
 }  // namespace

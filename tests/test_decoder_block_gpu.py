@@ -586,6 +586,65 @@ def test_block_against_the_oracle(n, oracle_mod):
     assert dmel.dmel_get_device_error(clear=True) == 0
 
 
+@pytest.mark.parametrize("n", [3, 20, 400])
+def test_calls_that_follow_at_once(n):
+    """Each call reads what the one before wrote and reuses its workspace: a chain of calls without a pause
+    gives the bits of the same calls one at a time."""
+    s, x, state = block_state(90 + n, n)
+    ws = workspace_for(s)
+    names = ("y", "n1", "stream", "ids", "wts", "moe", "n2", "sc")
+
+    def chain(sync):
+        kept, st = [], state.clone()
+        inp = x.clone()
+        for _ in range(12):
+            block_step(s, inp, st, ws) if not sync else stepwise(inp, st)
+            kept.append([s[k].clone() for k in names])
+            inp.copy_(s["moe"])
+        torch.cuda.synchronize()
+        return kept
+
+    def stepwise(inp, st):
+        old = {f: getattr(dmel, f) for f in ("dmel_shortconv", "dmel_add_rmsnorm", "dmel_route", "dmel_experts")}
+        for f, call in old.items():
+            setattr(dmel, f, lambda *a, _call=call, **kw: (torch.cuda.synchronize(), _call(*a, **kw), torch.cuda.synchronize()))
+        try:
+            block_step(s, inp, st, ws)
+        finally:
+            for f, call in old.items():
+                setattr(dmel, f, call)
+
+    start = {k: s[k].clone() for k in names}
+    runs = []
+    for sync in (True, False, False):
+        for k in names:
+            s[k].copy_(start[k])
+        runs.append(chain(sync))
+    for other in runs[1:]:
+        for a, b in zip(runs[0], other):
+            for k, p, q in zip(names, a, b):
+                assert torch.equal(p.view(torch.uint8), q.view(torch.uint8)), k
+    # without anything between: the residual stream through 40 norms, and one expert call after another
+    w, r = s["g1"], start["stream"].clone()
+    for _ in range(40):
+        dmel.dmel_add_rmsnorm(r, w, r, residual=start["stream"])
+    one = start["stream"].clone()
+    for _ in range(40):
+        dmel.dmel_add_rmsnorm(one, w, one, residual=start["stream"])
+        torch.cuda.synchronize()
+    assert torch.equal(r, one)
+    outs = [torch.empty_like(s["moe"]) for _ in range(8)]
+    xs = [torch.roll(x, i, 0).contiguous() for i in range(8)]
+    for a, b in zip(xs, outs):
+        dmel.dmel_experts(a, s["ids"], s["wts"], s["w_in"], s["w_out"], b, ws)
+    for a, b in zip(xs, outs):
+        alone = torch.empty_like(b)
+        torch.cuda.synchronize()
+        dmel.dmel_experts(a, s["ids"], s["wts"], s["w_in"], s["w_out"], alone, ws)
+        assert torch.equal(alone, b)
+    assert dmel.dmel_get_device_error(clear=True) == 0
+
+
 def test_block_in_graphs_and_on_other_streams():
     """Captured and replayed with new inputs, two graphs with a workspace each replayed at the same time on
     two streams, and calls on a stream that is not the current one: the same bits as eager calls."""
