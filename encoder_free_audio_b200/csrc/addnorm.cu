@@ -119,7 +119,8 @@ struct Scales {
 // takes the block (and its address is the same in every thread, which saves registers).
 // Two pieces and 32 registers: what bounds the rate is how many threads an SM holds (2,048) and
 // then, for e4m3, the instructions per value. 24,000 x 6144 bf16 with the stream in and out: 183 us,
-// 6.4 TB/s (64 registers 198 us, one piece 230 us); 12,800 rows into e4m3 by 128 columns: 100 us.
+// 6.4 TB/s (64 registers 198 us, one piece 230 us); 12,800 rows into e4m3 by 128 columns: 100 us (179
+// and 92 with the grids of launch_typed, launches under one another's ends).
 // With no more rows than SMs one piece is the shorter way (8 rows: 2.4 us against 3.0), and for fp32
 // rows, which have twice the bytes per piece, it is the faster one (1,601 x 5992: 25 us against 29).
 template <typename T, typename TO, int V, bool kWarpRows>
