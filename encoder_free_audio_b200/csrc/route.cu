@@ -147,9 +147,11 @@ __device__ __forceinline__ int lanes_per_group(int groups) {
 // The groups kept, a bit each. A group is rated by the sum of its two largest values (one where
 // there is only one). The values lie in shared memory, group g's from v + g (per + lanes_per_group):
 // that far apart, the lanes that walk the groups use different banks. *worst, *best: the lowest
-// rating kept, the highest left out, in lane 0.
+// rating kept, the highest left out. *size (where asked for): the largest sum of the magnitudes of a
+// group's two values, which bounds what their roundings move its rating by; the rating itself does
+// not, since a bias of each sign may cancel in it.
 template <typename F>
-__device__ __forceinline__ unsigned keep_groups(const F *v, const Settings &q, F *worst, F *best) {
+__device__ __forceinline__ unsigned keep_groups(const F *v, const Settings &q, F *worst, F *best, F *size = nullptr) {
   const int groups = q.r.n_groups, lane = threadIdx.x & 31, share = lanes_per_group(groups), mine = lane / share;
   F m1 = kNone, m2 = kNone;
   if (mine < groups) {
@@ -178,6 +180,7 @@ __device__ __forceinline__ unsigned keep_groups(const F *v, const Settings &q, F
   F lo = in ? rated : -(F)kNone, hi = in ? (F)kNone : rated;
   *worst = -warp_max(-lo);
   *best = warp_max(hi);
+  if (size) *size = warp_max((m1 > kNone ? abs(m1) : (F)0) + (m2 > kNone ? abs(m2) : (F)0));
   return __ballot_sync(kAll, in);
 }
 
@@ -419,10 +422,11 @@ __global__ void __launch_bounds__(32 * kWarps, blocks_per_sm(EPL)) route_kernel(
         if (e < E) narrow[e + ((e * q.inv_per) >> 20) * share] = fmaxf(v[i], kNone);  // (NaN: -inf)
       }
       __syncwarp();
-      float worst, best;
-      kept = keep_groups(narrow, q, &worst, &best);
-      // two scores a rating
-      unsure = best > kNone && !(worst - best > 4.0f * off + cut_of(1) * fmaxf(fabsf(worst), fabsf(best)));
+      float worst, best, size;
+      kept = keep_groups(narrow, q, &worst, &best, &size);
+      // Two ratings, each of two values that are off by a score's error and half a unit of their own, and
+      // a sum off by half a unit of itself: 4 off + 4 2^-24 size.
+      unsure = best > kNone && !(worst - best > 4.0f * off + cut_of(1) * size);
 #pragma unroll
       for (int i = 0; i < EPL; ++i) {
         const float x = bias ? v[i] : l[i];

@@ -225,6 +225,33 @@ def test_route_ties_go_to_the_lower_index(oracle_mod):
             check_route(steps, 8, oracle_mod, bias, sigmoid=sigmoid, groups=8, topk_groups=3)
 
 
+def cancelling_bias(size, groups, per):
+    """Each group's first expert at +size, the others at -size: its two largest values nearly cancel in its rating."""
+    bias = torch.full((groups, per), -size, device=DEV)
+    bias[:, 0] = size
+    return bias.flatten()
+
+
+@pytest.mark.parametrize("sigmoid", [True, False])
+@pytest.mark.parametrize("size", [100.0, 1e3, 1e4, 1e6])
+@pytest.mark.parametrize("groups,per,kept", [(2, 2, 1), (8, 2, 4), (16, 4, 5), (32, 8, 8)])
+def test_route_groups_whose_values_cancel(size, groups, per, kept, sigmoid, oracle_mod):
+    """A rating near zero from values far from it: what rounds is the values. At 1e4 and 1e6 the fp32 ratings put
+    groups of tens of these tokens in another order than the 64-bit ones."""
+    g = torch.Generator(device=DEV).manual_seed(int(size) + groups)
+    logits = torch.randn((400, groups * per), generator=g, device=DEV)
+    check_route(logits, min(6, kept * per), oracle_mod, cancelling_bias(size, groups, per), 0, sigmoid, groups, kept)
+
+
+def test_route_groups_whose_values_cancel_by_hand(oracle_mod):
+    """Sigmoids 0.590492 + 0.698044 = 1.288536 below 0.647484 + 0.641067 = 1.288552. Beside +-1000 fp32 steps are
+    6.1e-5, no value is within 7e-6 of a tie, and the first rating is the larger by one step."""
+    logits = torch.tensor([[0.366, 0.838, 0.608, 0.58]], device=DEV)
+    bias = torch.tensor([1000.0, -1000.0, 1000.0, -1000.0], device=DEV)
+    ids, _ = check_route(logits, 2, oracle_mod, bias, 0, True, 2, 1)
+    assert ids[0].tolist() == [2, 3]
+
+
 @pytest.mark.parametrize("sigmoid", [True, False])
 def test_route_values_fp32_cannot_tell_apart(sigmoid, oracle_mod):
     """Biases that cancel the scores to within fp32's rounding, either way: the 64-bit order holds."""
