@@ -500,7 +500,7 @@ dmel_status dmel_experts(const void *x, int64_t n_tokens, const int32_t *ids, co
   if (!aligned(x, 16) || !aligned(ids, 4) || !aligned(weights, 4) || !aligned(out, 16) || !aligned(w->w_in, 16) ||
       !aligned(w->w_out, 16))
     return DMEL_ERR_INVALID_ARG;
-  const size_t need = experts_workspace_bytes(n_tokens, slots, *w);
+  const size_t need = experts_workspace_need(n_tokens, slots, *w);
   if (!workspace || workspace_bytes < need || !aligned(workspace, 256)) return DMEL_ERR_INVALID_ARG;
   const size_t xb = (size_t)n_tokens * w->dim * 2, sb = (size_t)n_tokens * slots * 4;
   const size_t wb = (size_t)w->n_experts * w->dim * w->hidden * 2;

@@ -986,8 +986,33 @@ cudaError_t launch_sum(const Call &c, int64_t n_tokens, int *launches) {
 
 }  // namespace
 
-size_t experts_workspace_bytes(int64_t n_tokens, int slots, const dmel_expert_weights &w) {
+size_t experts_workspace_need(int64_t n_tokens, int slots, const dmel_expert_weights &w) {
   return layout(n_tokens, slots, w).total;
+}
+
+// A call of fewer tokens may need more: rows in fp32 up to kSmallSlots, partial sums of a split K. While a
+// call is run the same way its bytes grow with the tokens, so the largest counts of each way are enough.
+// From one way to the next the tiles grow or, with the same tiles, the splits get fewer: each way is
+// one range of counts, and its end is found by halving.
+size_t experts_workspace_bytes(int64_t n_tokens, int slots, const dmel_expert_weights &w) {
+  auto same = [&](const Config &a, int64_t t) {
+    const Config b = config(t, slots, w);
+    return a.small == b.small && a.tile_tokens == b.tile_tokens && a.splits == b.splits;
+  };
+  size_t most = 0;
+  for (int64_t first = 1; first <= n_tokens;) {
+    const Config c = config(first, slots, w);
+    int64_t last = first, beyond = n_tokens + 1;
+    while (beyond - last > 1) {
+      const int64_t mid = last + (beyond - last) / 2;
+      if (same(c, mid)) last = mid;
+      else beyond = mid;
+    }
+    const size_t need = experts_workspace_need(last, slots, w);
+    if (need > most) most = need;
+    first = last + 1;
+  }
+  return most;
 }
 
 cudaError_t launch_experts(const void *x, int64_t n_tokens, const int32_t *ids, const float *weights, int slots,

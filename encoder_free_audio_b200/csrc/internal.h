@@ -102,7 +102,9 @@ cudaError_t launch_route(const void *logits, int64_t n_tokens, dmel_dtype dtype,
                          const dmel_router &r, int32_t *ids, float *weights, int num_sms, cudaStream_t stream,
                          int *launches);
 
-// Experts' products: workspace bytes and the launch (arguments checked).
+// Experts' products: workspace bytes of a call, the largest over the calls of up to n_tokens, and the
+// launch (arguments checked).
+size_t experts_workspace_need(int64_t n_tokens, int slots, const dmel_expert_weights &w);
 size_t experts_workspace_bytes(int64_t n_tokens, int slots, const dmel_expert_weights &w);
 cudaError_t launch_experts(const void *x, int64_t n_tokens, const int32_t *ids, const float *weights, int slots,
                            const dmel_expert_weights &w, void *out, void *workspace, uint32_t *err, int num_sms,

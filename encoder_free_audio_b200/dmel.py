@@ -477,7 +477,7 @@ def dmel_route(logits, ids, weights, n_shared: int = 0, bias=None, scoring: int 
 
 
 def dmel_experts_workspace_size(n_tokens: int, slots: int, n_experts: int, dim: int, hidden: int) -> int:
-    """Device workspace bytes of dmel_experts."""
+    """Device workspace bytes of dmel_experts for up to n_tokens tokens."""
     return int(_lib().dmel_experts_workspace_size(int(n_tokens), int(slots),
                                                   ExpertWeights(int(n_experts), int(dim), int(hidden))))
 

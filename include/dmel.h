@@ -427,8 +427,9 @@ typedef struct {
   const void *w_out; /* bf16 [n_experts x hidden x dim] row-major */
 } dmel_expert_weights; /* device pointers, 16-byte aligned */
 
-/* Bytes of device workspace dmel_experts needs (0 for no tokens or sizes out of contract; the
- * weight pointers are not looked at). */
+/* Bytes of device workspace that dmel_experts needs for up to n_tokens tokens: never less for more
+ * tokens, so scratch for the largest batch serves every smaller one of the same slots and experts (0
+ * for no tokens or sizes out of contract; the weight pointers are not looked at). */
 size_t dmel_experts_workspace_size(int64_t n_tokens, int slots, const dmel_expert_weights *w);
 dmel_status dmel_experts(const void *x, int64_t n_tokens, const int32_t *ids, const float *weights, int slots,
                          const dmel_expert_weights *w, void *out, void *workspace, size_t workspace_bytes,

@@ -462,6 +462,18 @@ def test_experts_many_slots(n, slots, e, d, h):
     assert (out[(ids < 0).all(1)] == 0).all()
 
 
+@pytest.mark.parametrize("slots,e,d,h,most", [(6, 32, 1032, 136, 18), (1, 2, 4096, 264, 2048), (2, 3, 2056, 72, 300)])
+def test_experts_workspace_of_the_largest_batch(slots, e, d, h, most):
+    """One workspace, sized for the largest batch, for every smaller one: the bits of a workspace of the call's own."""
+    x, ids, w, w_in, w_out = expert_inputs(65, most, slots, e, d, h)
+    size = dmel.dmel_experts_workspace_size(most, slots, e, d, h)
+    ws = torch.full((size,), 0xFF, dtype=torch.uint8, device=DEV)
+    for n in sorted({1, 2, 5, 10, 11, 16, 17, 64 // slots, 64 // slots + 1, most // 2, most - 1, most}):
+        args = x[:n].contiguous(), ids[:n].contiguous(), w[:n].contiguous(), w_in, w_out
+        assert torch.equal(run_experts(*args, workspace=ws), run_experts(*args)), n
+    assert dmel.dmel_get_device_error(clear=True) == 0
+
+
 def test_experts_model_width(oracle_mod):
     """6144 columns, 1,024 hidden: one token's six experts, and a step of 20 tokens."""
     x, ids, w, w_in, w_out = expert_inputs(50, 20, 6, 8, 6144, 1024)

@@ -127,6 +127,30 @@ def test_experts_workspace_size(lib):
     assert need <= size(4096, 6, 32, 6144, 1024) <= need + 6 * 256 + 256
 
 
+# (slots, experts, dim, hidden) and the largest batch: rows in fp32 up to 64 slots; K in parts, in the small calls, in
+# tiles of 32, 128 and 256 tokens; neither
+BATCHES = [(6, 32, 6144, 1024, 300), (1, 2, 4096, 512, 2200), (2, 3, 2056, 72, 700), (3, 7, 2056, 520, 800),
+           (64, 5, 64, 24, 40), (1, 1, 65536, 8, 10000), (8, 258, 6144, 64, 700), (1, 1024, 24, 16, 3000)]
+
+
+@pytest.mark.parametrize("slots,e,d,h,most", BATCHES)
+def test_experts_workspace_of_a_batch_serves_smaller_ones(lib, slots, e, d, h, most):
+    sizes = [dmel.dmel_experts_workspace_size(t, slots, e, d, h) for t in range(most + 1)]
+    assert all(a <= b for a, b in zip(sizes, sizes[1:]))
+    w = dict(n_experts=e, dim=d, hidden=h, w_in=at(5), w_out=at(6))
+    fits = lambda t, size: experts(lib, w, n=t, slots=slots, workspace=at(4), size=size) != INVALID  # noqa: E731
+    assert all(fits(t, sizes[most]) for t in range(1, most + 1))
+    assert all(fits(t, sizes[t]) for t in range(1, most + 1))
+    # no more than the neediest of the batches
+    assert not all(fits(t, sizes[most] - 1) for t in range(1, most + 1))
+
+
+def test_experts_workspace_size_of_the_largest_calls(lib):
+    size = dmel.dmel_experts_workspace_size
+    assert size(1 << 30, 1, 1024, 65536, 65536) > (1 << 30) * 65536 * 4
+    assert size((1 << 30) // 64, 64, 1, 8, 8) > size(1 << 20, 64, 1, 8, 8)
+
+
 # ------------------------------------------------------------------------------ the binding refuses
 
 def test_binding_refuses_what_c_cannot_see(lib):
