@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import operator
 import os
 
 import numpy as np
@@ -392,7 +393,7 @@ class ExpertWeights(ctypes.Structure):
                [(k, ctypes.c_void_p) for k in ("w_in", "w_out")]
 
 
-_router = functools.lru_cache(maxsize=64)(Router)  # the argument struct of a router's settings
+_router = functools.lru_cache(maxsize=64)(Router)  # the argument struct of a router's settings, plain numbers
 
 
 def _refuse(where: str, what: str):
@@ -466,9 +467,12 @@ def dmel_route(logits, ids, weights, n_shared: int = 0, bias=None, scoring: int 
     if len(all_logits) != 2 or len(shape) != 2:
         _refuse(where, f"logits and ids: want two dimensions, got {tuple(all_logits)} and {tuple(shape)}")
     dt, dev = logits.dtype, logits.get_device()
+    n_shared = operator.index(n_shared)
     n, e = all_logits[0], all_logits[1] - n_shared
     shape = (n, shape[1])
-    r = _router(e, n_shared, shape[1] - n_shared, n_groups, topk_groups, scoring, int(renormalise), scale)
+    # numbers, not what holds them: the struct is looked up by value, and a tensor's changes
+    r = _router(e, n_shared, shape[1] - n_shared, operator.index(n_groups), operator.index(topk_groups),
+                operator.index(scoring), int(renormalise), float(scale))
     _run_on(dev, stream, where, _lib().dmel_route,
             logits.data_ptr() if logits.is_contiguous() else _addr(logits, where, "logits", dt, all_logits, dev), n,
             DMEL_F32 if dt is torch.float32 else _dtype_code(logits),

@@ -153,6 +153,23 @@ def test_experts_workspace_size_of_the_largest_calls(lib):
 
 # ------------------------------------------------------------------------------ the binding refuses
 
+def test_route_settings_held_in_tensors_are_read_at_each_call(monkeypatch):
+    """A scale or a count that the caller keeps in a tensor and changes there."""
+    seen = []
+    monkeypatch.setattr(dmel, "_run_on", lambda device, stream, where, entry, *args: seen.append(args[4]))
+    scale, groups = torch.tensor(2.5), torch.tensor(2)
+    for s, k in ((2.5, 2), (7.0, 4)):
+        scale.fill_(s)
+        groups.fill_(k)
+        dmel.dmel_route(torch.zeros(3, 8), torch.zeros(3, 2, dtype=torch.int32), torch.zeros(3, 2), scale=scale,
+                        n_groups=groups, topk_groups=groups)
+        assert (seen[-1].scale, seen[-1].n_groups, seen[-1].topk_groups) == (s, k, k)
+    for bad in (dict(n_groups=2.0), dict(n_shared=0.5), dict(scoring="1"), dict(scale=None)):
+        with pytest.raises(TypeError):
+            dmel.dmel_route(torch.zeros(3, 8), torch.zeros(3, 2, dtype=torch.int32), torch.zeros(3, 2), **bad)
+
+
+
 def test_binding_refuses_what_c_cannot_see(lib):
     f, b = torch.float32, torch.bfloat16
     x, w = torch.zeros(4, 64), torch.ones(64)
