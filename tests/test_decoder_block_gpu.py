@@ -160,6 +160,46 @@ def test_add_rmsnorm_more_rows_than_blocks(oracle_mod):
     assert ((out.double() - q).abs() <= (2.0 ** -4 + 2 * norm_bound(d) + 2.0 ** -22) * q.abs() + 2.0 ** -10).all()
 
 
+# more rows than a block each, three to a block and more (the blocks' largest grids at 148 SMs, by width and types)
+@pytest.mark.parametrize("dt,odt,block,n,d", [
+    (BF16, E4M3, 128, 3 * 1480 + 7, 5992), (BF16, E4M3, 0, 2 * 1480 + 1, 6144), (BF16, E4M3, 32, 2 * 9472 + 5, 1000),
+    (BF16, BF16, 0, 2 * 5920 + 77, 5992), (BF16, F32, 0, 2 * 5920 + 3, 6144), (BF16, BF16, 0, 2 * 37888 + 9, 1000),
+    (F32, E4M3, 128, 2 * 592 + 417, 5992), (F32, E4M3, 0, 2 * 592 + 1, 6144), (F32, E4M3, 64, 2 * 9472 + 3, 264),
+    (F32, F32, 0, 2 * 9472 + 3, 1000), (F32, BF16, 0, 2 * 9472 + 1, 264), (F32, F32, 0, 9472 + 99, 8200),
+    (BF16, E4M3, 0, 2 * 592 + 5, 16384), (BF16, BF16, 0, 5000, 264), (BF16, BF16, 0, 5000, 512), (BF16, E4M3, 64, 5000, 256),
+    # as many rows as SMs, and one more: another number of pieces per thread
+    (BF16, BF16, 0, 148, 6144), (BF16, BF16, 0, 149, 6144), (BF16, E4M3, 128, 148, 1000), (BF16, E4M3, 128, 149, 1000),
+    (BF16, E4M3, 0, 149, 264), (BF16, BF16, 0, 149, 8)])
+def test_add_rmsnorm_rows_of_a_prompt(dt, odt, block, n, d):
+    """Wide rows past the grid: a block walks its rows with barriers between. The stream in its own buffer, the rows
+    behind the call's as they were; against fp64 on the device."""
+    x, r, w = norm_inputs(n + d, n, d, dt)
+    if odt is E4M3:
+        x[::3, :8] *= 30.0
+    blocks, b = -(-d // (block or d)), norm_bound(d)
+    out = torch.full((n + 2, d), 7.0, device=DEV).to(odt)
+    rout, scales = torch.cat([r, r[:2]]), torch.full((n + 2, blocks), 9.0, device=DEV)
+    kw = dict(scales=scales[:n], scale_block=block) if odt is E4M3 else {}
+    dmel.dmel_add_rmsnorm(x, w, out[:n], residual=rout[:n], residual_out=rout[:n], eps=1e-5, **kw)
+    assert (out[n:].float() == 7.0).all() and torch.equal(rout[n:], r[:2]) and (scales[n:] == 9.0).all()
+    for i in range(0, n, 4096):  # (rows in parts: fp64 copies)
+        at = slice(i, min(i + 4096, n))
+        s = x[at].double() + r[at].double()
+        y = s * w.double() / torch.sqrt((s * s).mean(1, keepdim=True) + 1e-5)
+        assert ((rout[at].double() - s).abs() <= (HALF_STEP[dt] * 1.001 + 2.0 ** -24) * s.abs()).all()
+        if odt is not E4M3:
+            assert ((out[at].double() - y).abs() <= (HALF_STEP[odt] * 1.001 + b) * y.abs() + 1e-37).all()
+            continue
+        wide = torch.nn.functional.pad(y.abs(), (0, blocks * (block or d) - d)).view(-1, blocks, block or d)
+        sc = wide.amax(2).clamp(min=1e-30) / 448
+        assert ((scales[at].double() - sc).abs() <= (b + 2 * 2.0 ** -24) * sc).all()
+        q = y / sc.repeat_interleave(block or d, 1)[:, :d]
+        assert ((out[at].double() - q).abs() <= (2.0 ** -4 + 2 * b + 4 * 2.0 ** -24) * q.abs() + 2.0 ** -10).all()
+    if odt is dt:  # the normed rows over x
+        dmel.dmel_add_rmsnorm(x, w, x, residual=r, residual_out=r, eps=1e-5)
+        assert torch.equal(x, out[:n]) and torch.equal(r, rout[:n])
+
+
 # ------------------------------------------------------------------------------ routing
 
 def run_route(logits, k, bias=None, shared=0, **kw):
@@ -389,6 +429,30 @@ def test_route_many_tokens_and_rows_behind(oracle_mod):
     assert (ids[n:] == -7).all() and (w[n:] == 9.0).all()
 
 
+@pytest.mark.parametrize("e,groups,kept", [(64, 1, 1), (64, 8, 3), (300, 1, 1)])
+@pytest.mark.parametrize("sigmoid", [True, False])
+def test_route_second_tokens_of_a_warp(e, groups, kept, sigmoid, oracle_mod):
+    """More tokens than warps: 500 rows, each at many places of a prompt, have their ids and weights wherever they
+    stand. A third of them has values that only fp64 tells apart, a third groups that cancel."""
+    g = torch.Generator(device=DEV).manual_seed(e + groups)
+    base = torch.randn((500, e), generator=g, device=DEV)
+    n = 148 * 64 * 4 * 2 + 777
+    at = torch.randint(0, 500, (n,), generator=g, device=DEV)
+    plain = 0.1 * torch.randn(e, generator=g, device=DEV)
+    row = base[0].double()
+    score = torch.sigmoid(row) if sigmoid else torch.softmax(row, 0)
+    near = (1.0 - score).float()
+    base[100:250] = torch.where(torch.rand((150, e), generator=g, device=DEV) < 0.5, base[0],
+                                torch.nextafter(base[0], torch.full_like(base[0], 9.0)))
+    for bias in (plain, near, cancelling_bias(1e4, groups, e // groups)):
+        rid, rw = oracle_mod.route(f64(base), 0, 6, sigmoid, f64(bias), groups, kept)
+        ids, w = run_route(base[at], 6, bias, scoring=int(sigmoid), n_groups=groups, topk_groups=kept)
+        where = at.cpu().numpy()
+        np.testing.assert_array_equal(ids, rid[where])
+        spread = float(base.max() - base.min())
+        assert (np.abs(w - rw[where]) <= (2 * spread + 28) * 2.0 ** -24 * rw[where]).all()
+
+
 # ------------------------------------------------------------------------------ experts
 
 def expert_inputs(seed, n, slots, e, d, h, empty=0.0):
@@ -499,6 +563,78 @@ def test_experts_exact_on_integers():
         for j in range(slots):
             ref += w[:, j:j + 1].double() * torch.bmm(64 * up[:, j:j + 1], w_out[ids[:, j].long()].double())[:, 0]
         assert torch.equal(run_experts(x, ids, w, w_in, w_out), ref.float().to(BF16))
+
+
+def check_experts_on_device(x, ids, w, w_in, w_out):
+    """As check_experts, the formula in fp64 on the device, expert by expert."""
+    out = run_experts(x, ids, w, w_in, w_out)
+    (n, d), (e, h, _) = x.shape, w_out.shape
+    ref, spread, size = (torch.zeros((n, d), dtype=torch.float64, device=DEV) for _ in range(3))
+    for i in range(e):
+        t, j = torch.nonzero(ids == i, as_tuple=True)
+        if t.numel() == 0:
+            continue
+        xi, wi, wo, wt = x[t].double(), w_in[i].double(), w_out[i].double(), w[t, j].double()[:, None]
+        a, b = xi @ wi, xi.abs() @ wi.abs()
+        g, u = a[:, :h], a[:, h:]
+        hid = g * torch.sigmoid(g) * u
+        y = wt * (hid @ wo)
+        sums = (d / 16 + 16) * 2.0 ** -23
+        dh = 2.0 ** -8 * hid.abs() + sums * (1.1 * b[:, :h] * u.abs() + g.abs() * b[:, h:])
+        ref.index_add_(0, t, y)
+        size.index_add_(0, t, y.abs())
+        spread.index_add_(0, t, wt.abs() * ((dh + (h / 16 + 16) * 2.0 ** -23 * hid.abs()) @ wo.abs()))
+    off = (out.double() - ref).abs()
+    sums = ids.shape[1] * 2.0 ** -23 * ref.abs() + 2.0 ** -11 * size
+    assert (off <= 2.0 ** -8 * 1.01 * ref.abs() + 1.01 * spread + sums + 1e-37).all()
+    assert off.norm() <= 1.25 * 2 ** 0.5 * 2.0 ** -8 / 3 ** 0.5 * ref.norm()
+    assert (out[(ids < 0).all(1)] == 0).all()
+    assert dmel.dmel_get_device_error(clear=True) == 0
+    return out
+
+
+@pytest.mark.parametrize("n,slots,e,d,h", [
+    (14000, 2, 5, 2056, 600), (19000, 1, 1, 2048, 520),   # tiles of twice the columns, with a remainder of columns
+    (30000, 5, 3, 72, 40), (20000, 6, 32, 136, 72), (1500, 1, 1000, 16, 8)])  # plans of several blocks and batches
+def test_experts_many_slots_value_by_value(n, slots, e, d, h):
+    check_experts_on_device(*expert_inputs(n, n, slots, e, d, h, empty=0.1))
+
+
+@pytest.mark.parametrize("n,slots,e,d,h", [(14000, 2, 5, 2056, 600), (30000, 5, 3, 72, 40), (20000, 6, 32, 136, 72),
+                                           (4000, 17, 300, 80, 56)])
+def test_experts_many_slots_exact_on_integers(n, slots, e, d, h):
+    """As test_experts_exact_on_integers, at tiles of twice the columns and plans of several blocks and batches: a slot's
+    values are 64 times whole numbers up to 600, which 11 bits hold."""
+    g = torch.Generator(device=DEV).manual_seed(n)
+    at = torch.randint(0, d, (n,), generator=g, device=DEV)
+    x = torch.nn.functional.one_hot(at, d).to(BF16)
+    w_in = torch.randint(-1, 2, (e, d, 2 * h), generator=g, device=DEV).to(BF16)
+    w_in[:, :, :h] = 64.0
+    w_out = torch.randint(-1, 2, (e, h, d), generator=g, device=DEV).to(BF16)
+    ids = torch.randint(-1, e, (n, slots), generator=g, device=DEV, dtype=torch.int32)
+    w = 2.0 ** torch.randint(-1, 2, (n, slots), generator=g, device=DEV)
+    ref = torch.zeros((n, d), dtype=torch.float64, device=DEV)
+    for i in range(e):
+        t, j = torch.nonzero(ids == i, as_tuple=True)
+        ref.index_add_(0, t, w[t, j].double()[:, None] * (64 * w_in[i, at[t], h:].double() @ w_out[i].double()))
+    assert torch.equal(run_experts(x, ids, w, w_in, w_out), ref.float().to(BF16))
+
+
+@pytest.mark.parametrize("n", [1, 8, 64, 600])
+def test_experts_as_the_router_feeds_them(n):
+    """256 routed experts, 6 chosen, and 2 shared ones that every token takes, 6144 columns and 1,024 hidden: tiles of
+    many tokens beside tiles of one or two."""
+    e, d, h = 258, 6144, 1024
+    g = torch.Generator(device=DEV).manual_seed(n)
+    weight = lambda *shape: torch.empty(shape, dtype=BF16, device=DEV).normal_(0.0, shape[1] ** -0.5, generator=g)  # noqa: E731
+    w_in, w_out = weight(e, d, 2 * h), weight(e, h, d)
+    x = torch.randn((n, d), generator=g, device=DEV).to(BF16)
+    ids = torch.empty((n, 8), dtype=torch.int32, device=DEV)
+    w = torch.empty((n, 8), device=DEV)
+    logits = torch.randn((n, e), generator=g, device=DEV)
+    dmel.dmel_route(logits, ids, w, n_shared=2, bias=0.05 * torch.randn(e - 2, generator=g, device=DEV))
+    assert (ids[:, 6:] == torch.tensor([256, 257], device=DEV)).all()
+    check_experts_on_device(x, ids, w, w_in, w_out)
 
 
 def test_experts_empty_slots_and_bad_ids(oracle_mod):
@@ -731,3 +867,52 @@ def test_block_in_graphs_and_on_other_streams():
         for s, state, buf, xs, want, graph, first, ws in runs:
             assert same(s, want[i]), i
     del runs
+
+
+def test_block_captured_behind_a_join_of_streams():
+    """Calls captured right behind a copy and behind the join of another stream, where a launch has several
+    predecessors of several kinds: the same bits as eager calls, for new inputs too."""
+    s, x, state = block_state(82, 29)
+    ws = workspace_for(s)
+    buf, other = x.clone(), torch.empty_like(s["stream"])
+    side = torch.cuda.Stream()
+    first = s["stream"].clone()
+
+    def calls(main):
+        # the norm behind the join of a copy on the side and the stream's own copy
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            other.copy_(first)
+            other.mul_(2)
+        s["y"].copy_(buf)
+        main.wait_stream(side)
+        dmel.dmel_add_rmsnorm(s["y"], s["g1"], s["n1"], residual=other, residual_out=s["stream"])
+        # the router on the side, the experts behind its join
+        logits = torch.matmul(s["n1"], s["router"]).float()
+        side.wait_stream(main)
+        dmel.dmel_route(logits, s["ids"], s["wts"], n_shared=2, bias=s["bias"], stream=side)
+        s["moe"].zero_()
+        main.wait_stream(side)
+        dmel.dmel_experts(s["n1"], s["ids"], s["wts"], s["w_in"], s["w_out"], s["moe"], ws)
+        dmel.dmel_add_rmsnorm(s["moe"], s["g2"], s["n2"], residual=s["stream"], residual_out=s["stream"], scales=s["sc"],
+                              scale_block=128)
+        return logits  # (kept: the side stream reads it)
+
+    names = ("n1", "stream", "ids", "wts", "moe", "n2", "sc")
+    want, inputs = [], (x, torch.roll(x, 1, 0), torch.roll(x, 2, 0))
+    for xi in inputs:
+        buf.copy_(xi)
+        keep = calls(torch.cuda.current_stream())
+        torch.cuda.synchronize()
+        want.append([s[k].clone() for k in names])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        keep = calls(torch.cuda.current_stream())  # noqa: F841
+    for _ in range(2):
+        for xi, old in zip(inputs, want):
+            buf.copy_(xi)
+            graph.replay()
+            torch.cuda.synchronize()
+            for k, v in zip(names, old):
+                assert torch.equal(s[k].view(torch.uint8), v.view(torch.uint8)), k
+    assert dmel.dmel_get_device_error(clear=True) == 0
