@@ -261,7 +261,9 @@ template <typename T, typename TO>
 cudaError_t launch_typed(const void *x, const void *res, int64_t n_rows, int dim, const void *w, float eps,
                          void *res_out, void *out, Scales sc, int num_sms, cudaStream_t stream) {
   const int pieces = dim / 8;
-  const bool two = pieces > 1024 || (sizeof(T) == 2 && n_rows > num_sms);
+  // (A row of 32 pieces or less has one per lane of its warp either way: 24,000 x 256 bf16 take 8.4 us,
+  // with an empty second piece 10.6.)
+  const bool two = pieces > 1024 || (sizeof(T) == 2 && n_rows > num_sms && pieces > 32);
   const int threads = ((two ? (pieces + 1) / 2 : pieces) + 31) / 32 * 32;
   const bool warp_rows = threads == 32;
   const dim3 block(threads, warp_rows ? 8 : 1);
@@ -282,8 +284,10 @@ cudaError_t launch_typed(const void *x, const void *res, int64_t n_rows, int dim
   const cudaLaunchConfig_t cfg = programmatic_launch(grid, block, 0, stream, &at);
 #define DMEL_NORM(V, ROWS) \
   return cudaLaunchKernelEx(&cfg, add_rmsnorm_kernel<T, TO, V, ROWS>, xt, rt, n_rows, dim, wt, eps, so, ot, sc)
-  if (warp_rows && two) DMEL_NORM(2, true);
-  else if (warp_rows) DMEL_NORM(1, true);
+  if constexpr (sizeof(T) == 2) {  // (fp32 rows of two pieces are wider than a warp)
+    if (warp_rows && two) DMEL_NORM(2, true);
+  }
+  if (warp_rows) DMEL_NORM(1, true);
   else if (two) DMEL_NORM(2, false);
   else DMEL_NORM(1, false);
 #undef DMEL_NORM
