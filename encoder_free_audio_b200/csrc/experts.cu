@@ -3,9 +3,10 @@
 //     out[t] = sum_j weights[t, j] (silu(x[t] G_e) * (x[t] U_e)) D_e,   e = ids[t, j].
 //
 // Four steps: a plan (the slots ordered by expert, cut into tiles of tokens), the gate and up
-// products with the gating in the epilogue, the down product, and each token's weighted sum. Up to
-// kSmallSlots slots take two launches: every block of the first product makes the plan itself, and
-// the last block of the second to finish some columns sums them. More take one launch each.
+// products with the gating in the epilogue, the down product, and each token's weighted sum. With more
+// than kSmallSlots slots each has a launch. Up to that, the last block of the down product to finish
+// some columns sums them, and every block of the first product makes the plan itself: two launches;
+// or three, with the plan's own, where K of the first product is split.
 //
 // Both products run on the tensor cores with the roles swapped: an expert's weights are the M
 // side (256 weight columns per pair of CTAs) and its tokens the N side, whose size an MMA takes in
@@ -13,10 +14,12 @@
 // with 700 costs three tiles of about 240, and no tile is padded by more than 15 tokens.
 //
 // A product kernel is persistent, one CTA pair per two SMs: a TMA warp loads weight boxes (64
-// columns x 64 K, MN-major, 128-byte swizzle) and gathers token rows four at a time (K-major) by
-// their index, so tokens are never copied into expert order; one thread issues M = 256, K = 16
-// MMAs into a double-buffered TMEM accumulator; four warps move finished accumulators (a lane per
-// weight column) through shared memory into rows.
+// columns x 64 K, MN-major, 128-byte swizzle) and, for the down product, the gated rows, which lie in
+// expert order; two or eight gather warps of the first product load token rows four at a time
+// (K-major) by their index, so tokens are never copied into that order; an elected lane of one warp
+// issues M = 256, K = 16 MMAs into TMEM, which holds two tiles' accumulators (or one tall tile's: its
+// two halves are the two sets of columns); eight warps, in two groups of four, move finished
+// accumulators (a lane per weight column) through shared memory into rows.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -42,8 +45,8 @@ struct TokenTile {
 // The slots in expert order, stable, by counting: a warp counts its chunk of slots per expert, a
 // scan over (expert, block, warp) turns the counts into row numbers, and the same walk hands them
 // out. Bound by the matching of 32 slots at a time (about 190 cycles of a scheduler each): one
-// block for few slots, else a cluster of eight that read each other's counts (24,576 slots: 11 us,
-// with one block 38).
+// block for few slots, else a cluster of eight that read each other's counts (24,576 slots: 10 us,
+// with one block 48).
 constexpr int kPlanThreads = 1024;
 constexpr int kAhead = 8;  // slots per lane whose ids are loaded before any is counted
 
@@ -200,9 +203,10 @@ __global__ void __launch_bounds__(kPlanThreads) experts_plan_kernel(const Shared
 // The same for at most kSmallSlots slots, by every block of the first product for itself in shared
 // memory, by comparing each slot with all others. The `writer` block also leaves it in memory for
 // the second product, and clears its counters. With the sums in the second product that saves two
-// launches: one token's 6 slots 49.5 us against 53 (before what came later to both). With 384 slots both cost more than the launches
-// (277 us against 208: the comparisons, and a fence per tile; a plan by counting in every block, 31 us
-// against 29 for 128 slots of 2048 x 512).
+// launches, which both cost more than with many slots: the comparisons, and a fence per work item. 6
+// slots a token on 32 experts, 6144 x 1024: 6 slots 46 us against 49, 24 slots 110 against 111, 60 slots
+// 185 against 181, 66 slots 190 against 184, 192 slots 220 against 202; 128 slots on 8 experts,
+// 2048 x 512: 32 against 23. (Up to here the slots' rows stay in fp32 as well.)
 constexpr int kSmallSlots = 64;
 
 struct SmallPlan {
@@ -314,32 +318,16 @@ struct EX {
   static_assert(N_BARS * 8 + 8 <= 504 && SMEM_BYTES <= 227 * 1024, "shared memory budget");
 };
 
-// Barrier of 128 threads by number; and one that also ANDs a flag, so that all take the same branch.
-__device__ __forceinline__ void group_bar(int id) { asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory"); }
-__device__ __forceinline__ bool group_bar_and(int id, bool v) {
-  uint32_t out;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.u32 p, %1, 0;\n\t"
-      "bar.red.and.pred q, %2, 128, p;\n\t"
-      "selp.u32 %0, 1, 0, q;\n\t}\n"
-      : "=r"(out)
-      : "r"((uint32_t)v), "r"(id)
-      : "memory");
-  return out != 0;
+// Barrier of an epilogue group's 128 threads; and one that also ANDs a flag, so that all take the same branch.
+__device__ __forceinline__ void group_bar(int group) { asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory"); }
+__device__ __forceinline__ bool group_bar_and(int group, bool v) {
+  return group == 0 ? group_and<1, 128>(v) : group_and<2, 128>(v);
 }
 
 __device__ __forceinline__ float4 silu_times(float4 g, float4 u) {
   // __expf and __fdividef are within a few fp32 ulps here; the result is rounded to bf16
   return make_float4(__fdividef(g.x, 1.0f + __expf(-g.x)) * u.x, __fdividef(g.y, 1.0f + __expf(-g.y)) * u.y,
                      __fdividef(g.z, 1.0f + __expf(-g.z)) * u.z, __fdividef(g.w, 1.0f + __expf(-g.w)) * u.w);
-}
-
-// The warp's largest value, in one instruction.
-__device__ __forceinline__ float warp_max(float v) {
-  float m;
-  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
-  return m;
 }
 
 // The power of two that takes a block's largest magnitude to [2^14, 2^15), inside fp16's range with
@@ -611,7 +599,7 @@ __global__ void __launch_bounds__(kGate ? EX<kTokens, kSmall, kTall>::THREADS_GA
     }
   } else if (kGate && warp >= 2 + X::EPI_WARPS) {
     // ------------------------------------------------ gather: token rows four at a time, by number
-    // Gather warp w takes every other group of four rows of this CTA's half.
+    // Gather warp w takes the groups of four rows w, w + GATHER_WARPS, ... of this CTA's half.
     const int w = warp - 2 - X::EPI_WARPS;
     int4 *idx = reinterpret_cast<int4 *>(smem + X::OFF_IDX);
     int stage = 0;
@@ -662,7 +650,7 @@ __global__ void __launch_bounds__(kGate ? EX<kTokens, kSmall, kTall>::THREADS_GA
       const uint32_t acc = i % X::ACCS, use = i / X::ACCS;
       const TokenTile tt = token_tile(t);
       const int first_col = column(t);
-      ok = group_bar_and(1 + group, ok && mbar_wait(tfull(acc), use & 1u, err));
+      ok = group_bar_and(group, ok && mbar_wait(tfull(acc), use & 1u, err));
       tc_fence_after();
       // chunks of both sets, the sets one after the other
       const int per_set = (tt.width + X::STG_TOKENS - 1) / X::STG_TOKENS;
@@ -683,7 +671,7 @@ __global__ void __launch_bounds__(kGate ? EX<kTokens, kSmall, kTall>::THREADS_GA
 #pragma unroll
           for (int k = 0; k < 16; ++k) buf[(16 + k) * 128 + m] = __uint_as_float(v[1][k]);
         }
-        group_bar(1 + group);
+        group_bar(group);
         const int n_tok = tt.rows - c < 32 ? tt.rows - c : 32;
         if (kSplit) {
           float *part = shared.partial + ((t * 2 + rank) * kTokens + c) * 128 + 4 * (et & 31);
@@ -742,7 +730,7 @@ __global__ void __launch_bounds__(kGate ? EX<kTokens, kSmall, kTall>::THREADS_GA
             }
           }
         }
-        group_bar(1 + group);  // the buffer has been read
+        group_bar(group);  // the buffer has been read
       }
       tc_fence_before();
       __syncwarp();
@@ -823,9 +811,12 @@ Config config(int64_t n_tokens, int slots, const dmel_expert_weights &w) {
   Config c;
   const int64_t n = n_tokens * slots;
   // Tiles of 32 tokens (ten stages of weights in flight) where an expert has few on average: the
-  // weights' bytes and latency bound such calls (128 slots on 8 experts, 2048 / 512: 29 us, 33 with
-  // tiles of 128, 35 with 256). Wider ones share a pass over the weights between their tokens (1,536
-  // slots on 32 experts, 6144 / 1024: 335, 218 and 221 us; 6,144 slots: 1,014, 406 and 319 us).
+  // weights' bytes and latency bound such calls. Wider ones share a pass over the weights between
+  // their tokens. 6 slots a token on 32 experts, 6144 / 1024, tiles of 32, 128 and 256: 1,536 slots 320,
+  // 213 and 213 us; 6,144 slots 1,008, 383 and 258. Since a tile loads only the rows that are there,
+  // 32 gains little over 128 (128 slots on 8 experts, 2048 / 512: 23 us each), and it loses where the
+  // mean is no guide: 8 slots a token on 258 experts, two of them shared by all tokens, 64 tokens 1,137
+  // us for 1,078, 512 tokens 1,624 for 1,436.
   c.tile_tokens = n <= kSmallSlots || n <= 16 * (int64_t)w.n_experts ? 32 : n <= 64 * (int64_t)w.n_experts ? 128 : 256;
   c.max_tiles = n / c.tile_tokens + (n < w.n_experts ? n : w.n_experts);
   // The first product's K in up to 8 parts of 16 blocks or more where its tiles would leave half of

@@ -186,6 +186,12 @@ __device__ __forceinline__ void epi_bar() { asm volatile("bar.sync 1, %0;" ::"n"
 
 __device__ __forceinline__ void gather_bar() { asm volatile("bar.sync 2, 128;" ::: "memory"); }
 
+__device__ __forceinline__ float4 lds4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
+  return v;
+}
+
 // TMA bulk tensor store of a 2D box from shared memory (no multicast), and its bulk-group
 // bookkeeping: commit, wait until the source may be overwritten (.read) or until done.
 __device__ __forceinline__ void tma_store_2d(const void *tmap, int32_t x, int32_t y, uint32_t src) {

@@ -15,7 +15,9 @@
 // one in five hundred of ordinary logits) has the winners and what is near the last of them ordered
 // by their scores in fp64, one candidate a lane: 1.5 us with sigmoids, 2.7 with a softmax, whose sum
 // is wanted too. All experts are chosen again in fp64 (6 to 8 us) only where two groups are that near
-// or more than 32 candidates are.
+// or more than 32 candidates are. So the time goes by the logits: 12,800 bf16 rows of 256 in 8 groups
+// without a bias take 25 us where they are normal draws and 68 where all are zeros, as padding is;
+// 24,000 fp32 rows without groups or bias 17 and 34.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math_constants.h>
@@ -88,17 +90,6 @@ __device__ __forceinline__ float fast_rcp(float x) {
   return y;
 }
 
-// The warp's largest value, in one instruction.
-__device__ __forceinline__ float warp_max(float v) {
-  float m;
-  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
-  return m;
-}
-__device__ __forceinline__ double warp_max(double v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(kAll, v, o));
-  return v;
-}
 template <typename F>
 __device__ __forceinline__ F warp_sum(F v) {
 #pragma unroll
@@ -477,7 +468,9 @@ __global__ void __launch_bounds__(32 * kWarps, blocks_per_sm(EPL)) route_kernel(
       }
     }
     // weights. Renormalised: s / sum(s) from values scaled by exp(-m), m the largest chosen logit
-    // (sigmoid: where it is negative), so that scores too small for a float keep their ratios.
+    // (sigmoid: where it is negative), so that scores too small for a float keep their ratios. All in
+    // fp32, with expf (a unit or two) and a division by approximate reciprocal (two units) of a number
+    // in (1, 2]: the weights are fp32, and what they order is settled above.
     float m = sigmoid ? 0.0f : top;
     if (r.renormalise) {
       m = warp_max(x);

@@ -379,7 +379,8 @@ dmel_status dmel_add_rmsnorm(const void *x, const void *residual, int64_t n_rows
  *   weights  s of the chosen (without the bias), divided by their sum when renormalise is not 0,
  *            times scale
  * The choice is made as 64-bit arithmetic makes it: values that fp32 cannot tell apart are compared
- * again in fp64. An expert whose logit is -inf or NaN is never chosen; a slot left without an
+ * again in fp64 (which takes time: tokens whose groups or values are nearly equal, such as padding
+ * rows of equal logits, cost up to three times what others do). An expert whose logit is -inf or NaN is never chosen; a slot left without an
  * expert (a masked token, a masked shared expert) has id -1 and weight 0. +inf counts as FLT_MAX.
  * A NaN in bias counts as -inf there.
  * logits   [n_tokens x (n_experts + n_shared)] in dtype (fp32 or bf16), device, aligned to dtype
@@ -418,7 +419,7 @@ dmel_status dmel_route(const void *logits, int64_t n_tokens, dmel_dtype dtype, c
  * operand), with more than 64 slots each expert's output row to 11 bits beside a scale per 128
  * columns, and the token's fp32 sum to bf16. How tokens are batched changes no more than that
  * rounding and the order of fp32 sums.
- * n_tokens * slots at most 2^30. Asynchronous on stream; two to four launches, by the number of slots. */
+ * n_tokens * slots at most 2^30. Asynchronous on stream; two to four launches, by the sizes. */
 typedef struct {
   int n_experts;     /* 1 .. 1024 */
   int dim;           /* model width, a positive multiple of 8, at most 65536 */
